@@ -60,6 +60,36 @@ class mk_kv_cache(ctypes.Structure):
     _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p)]
 
 
+class mk_kv_pool(ctypes.Structure):
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("n_layers", ctypes.c_int32),
+                ("n_pages", ctypes.c_int32), ("n_kv_heads", ctypes.c_int32), ("page", ctypes.c_int32),
+                ("head_dim", ctypes.c_int32), ("elem_bytes", ctypes.c_int32)]
+
+
+class mk_kv_state(ctypes.Structure):
+    _fields_ = [("words", ctypes.c_void_p), ("n_seqs", ctypes.c_int32), ("max_pages", ctypes.c_int32),
+                ("n_pages", ctypes.c_int32)]
+
+
+class mk_attn_shared_args(ctypes.Structure):
+    _fields_ = ([(n, ctypes.c_int32) for n in ("batch", "n_tokens", "n_q_heads", "n_kv_heads", "head_dim", "dtype",
+                                               "page", "n_pages", "n_prefix_pages", "table_width")] +
+                [("scale", ctypes.c_float)] +
+                [(n, ctypes.c_void_p) for n in ("q", "k", "v", "out", "lse", "prefix_pages", "prefix_len", "table",
+                                                "lens", "status")] +
+                [(n, ctypes.c_int64) for n in ("q_batch_stride", "q_token_stride", "q_head_stride",
+                                               "out_batch_stride", "out_token_stride", "out_head_stride",
+                                               "page_stride", "kv_head_stride", "row_stride")])
+
+
+class mk_verify_args(ctypes.Structure):
+    _fields_ = ([(n, ctypes.c_int32) for n in ("batch", "max_drafted", "vocab")] +
+                [(n, ctypes.c_void_p) for n in ("target", "draft", "tokens", "n_drafted", "u", "out_tokens",
+                                                "n_accepted", "status")] +
+                [(n, ctypes.c_int64) for n in ("target_batch_stride", "target_row_stride", "draft_batch_stride",
+                                               "draft_row_stride")])
+
+
 class mk_plan_opts(ctypes.Structure):
     _fields_ = [("batch", ctypes.c_int32), ("kv_splits", ctypes.c_int32), ("sched_mode", ctypes.c_int32),
                 ("exec_mode", ctypes.c_int32), ("num_sms", ctypes.c_int32), ("trace", ctypes.c_int32),
@@ -153,6 +183,28 @@ def load(path: str = LIB_PATH):
                                         P(mk_cost_estimate), ctypes.c_char_p, sz]
     L.mk_host_plan_simulate.restype = i32
     L.mk_host_plan_simulate.argtypes = [P(mk_config), P(mk_plan_opts), i32, i32, u64, i32, ctypes.c_char_p, sz]
+    L.mk_kv_state_words.restype = i64
+    L.mk_kv_state_words.argtypes = [i32, i32, i32]
+    L.mk_kv_workspace_bytes.restype = i64
+    L.mk_kv_workspace_bytes.argtypes = [i32, i32]
+    L.mk_kv_init.restype = i32
+    L.mk_kv_init.argtypes = [P(mk_kv_state), vp]
+    L.mk_kv_resize.restype = i32
+    L.mk_kv_resize.argtypes = [P(mk_kv_pool), P(mk_kv_state), vp, vp, i32, vp, vp]
+    L.mk_kv_fork.restype = i32
+    L.mk_kv_fork.argtypes = [P(mk_kv_pool), P(mk_kv_state), vp, vp, i32, vp, vp]
+    L.mk_kv_compact.restype = i32
+    L.mk_kv_compact.argtypes = [P(mk_kv_pool), P(mk_kv_state), vp, vp]
+    L.mk_kv_copy.restype = i32
+    L.mk_kv_copy.argtypes = [P(mk_kv_pool), P(mk_kv_pool), vp, i32, vp, vp, vp]
+    L.mk_attn_shared_workspace_bytes.restype = i64
+    L.mk_attn_shared_workspace_bytes.argtypes = [P(mk_attn_shared_args)]
+    L.mk_attn_shared.restype = i32
+    L.mk_attn_shared.argtypes = [P(mk_attn_shared_args), vp, vp]
+    L.mk_token_probs.restype = i32
+    L.mk_token_probs.argtypes = [vp, i32, i64, vp, vp, i64, i32, i32, vp]
+    L.mk_verify.restype = i32
+    L.mk_verify.argtypes = [P(mk_verify_args), vp]
     _lib = L
     return L
 

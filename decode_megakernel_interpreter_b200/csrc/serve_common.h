@@ -1,0 +1,72 @@
+// Shared by the serving operators' translation units (declared in
+// include/mk_serve.h): error mapping, launches with programmatic dependent
+// launch, and the status word.
+#pragma once
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include "../../include/mk_serve.h"
+
+namespace mk {
+
+inline int serve_code(cudaError_t e) {
+  if (e == cudaSuccess) return MK_OK;
+  cudaGetLastError();
+  if (e == cudaErrorMemoryAllocation) return MK_ERR_OUT_OF_MEMORY;
+  if (e == cudaErrorLaunchOutOfResources || e == cudaErrorInvalidConfiguration) return MK_ERR_LAUNCH;
+  return MK_ERR_CUDA;
+}
+
+// Launch fn; `overlap`: its blocks may start while the kernel before it on
+// the stream drains (the kernel then calls pdl_wait before it touches what
+// that one wrote); `cluster` > 1: blocks of a cluster.
+template <class... A, class... B>
+int serve_launch(void (*fn)(A...), dim3 grid, int threads, size_t smem, cudaStream_t st, bool overlap, int cluster,
+                 B... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3((unsigned)threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cudaLaunchAttribute at[2];
+  int n = 0;
+  if (overlap) {
+    at[n].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[n++].val.programmaticStreamSerializationAllowed = 1;
+  }
+  if (cluster > 1) {
+    at[n].id = cudaLaunchAttributeClusterDimension;
+    at[n].val.clusterDim.x = (unsigned)cluster;
+    at[n].val.clusterDim.y = 1;
+    at[n++].val.clusterDim.z = 1;
+  }
+  cfg.attrs = at;
+  cfg.numAttrs = (unsigned)n;
+  return serve_code(cudaLaunchKernelEx(&cfg, fn, static_cast<A>(args)...));
+}
+
+inline bool aligned_to(const void *p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
+
+#ifdef __CUDACC__
+namespace {
+// The kernel before this one on the stream has finished and its writes are visible.
+__device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+// The next kernel's blocks may be scheduled.
+__device__ __forceinline__ void pdl_trigger() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+// First code wins.
+__device__ __forceinline__ void report(int32_t *status, int code) {
+  if (status) atomicCAS(status, 0, code);
+}
+__device__ __forceinline__ int warp_incl_sum(int v) {
+  const int lane = threadIdx.x & 31;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int t = __shfl_up_sync(0xffffffffu, v, o);
+    if (lane >= o) v += t;
+  }
+  return v;
+}
+}  // namespace
+#endif
+
+}  // namespace mk

@@ -5,13 +5,17 @@
 // form one matrix, so a prefix tile is read once and multiplied by all of
 // them; the own parts are small matrices of n_tokens * group rows each.  Both
 // give partial results (unnormalised o, row maximum m, row sum l), which a
-// second kernel joins:
+// last kernel joins:
 //   o = sum_s 2^(m_s - M) o_s / sum_s 2^(m_s - M) l_s,  M = max_s m_s.
+// A sequence one of whose queries ends inside the prefix does not share it:
+// its whole length is then its own part, so that the shared part has no masks
+// but the prefix's end.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
 #include <algorithm>
 #include <cmath>
+#include <type_traits>
 
 #include "serve_common.h"
 
@@ -37,6 +41,11 @@ struct AttnDev {
   int n_prefix_items, own_tiles, n_items;  // items: prefix [kv head][row tile], then own [b][kv head][row tile]
   float *part_o;    // [slot][kRows][d]
   float2 *part_ml;  // [slot][kRows]
+  // the prefix on the tensor cores (tc_rows > 0; n_prefix_items is 0 then):
+  // items [kv head][group of tc_rows rows]
+  int tc_rows, tc_groups;
+  float4 *tc_o;    // [slot][half][d / 4][kTcRows]
+  float2 *tc_ml;   // [slot][half][kTcRows]
 };
 
 // The work as a line of K/V tiles: item i owns tiles [start(i), start(i + 1));
@@ -56,16 +65,26 @@ __device__ __forceinline__ int seq_len(const AttnDev &p, int b) {
   if (n > cap) report(p.status, MK_ERR_DEVICE_INPUT);
   return min(n, cap);
 }
-__device__ __forceinline__ int own_len(const AttnDev &p, int b, int prefix) { return max(0, seq_len(p, b) - prefix); }
+// whether every query of sequence b sees the whole prefix
+__device__ __forceinline__ bool shares(const AttnDev &p, int b, int prefix) {
+  return prefix > 0 && seq_len(p, b) - (p.T - 1) >= prefix;
+}
+// the own part of sequence b begins here, and has this many positions
+__device__ __forceinline__ int own_start(const AttnDev &p, int b, int prefix) { return shares(p, b, prefix) ? prefix : 0; }
+__device__ __forceinline__ int own_len(const AttnDev &p, int b, int prefix) {
+  return max(0, seq_len(p, b) - own_start(p, b, prefix));
+}
+__device__ __forceinline__ int prefix_of(const AttnDev &p) {
+  const long long cap = (long long)p.n_prefix_pages * p.page, n = p.n_prefix_pages > 0 ? p.prefix_len[0] : 0;
+  if ((n < 0 || n > cap) && threadIdx.x == 0) report(p.status, MK_ERR_DEVICE_INPUT);
+  return (int)max(0ll, min(n, cap));
+}
 
 // Tiles of one own item of each sequence as prefix sums: sum[b] = tiles of the
 // sequences before b (sum: B + 1 ints).  Called by the whole block.
 __device__ Line make_line(const AttnDev &p, int blocks, int *sum, int *red) {
   Line l;
-  const long long cap = (long long)p.n_prefix_pages * p.page;
-  long long n = p.n_prefix_pages > 0 ? p.prefix_len[0] : 0;
-  if ((n < 0 || n > cap) && threadIdx.x == 0) report(p.status, MK_ERR_DEVICE_INPUT);
-  l.prefix = (int)max(0ll, min(n, cap));
+  l.prefix = prefix_of(p);
   l.prefix_tiles = (l.prefix + kKeys - 1) / kKeys;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, per = (p.B + blockDim.x - 1) / blockDim.x;
   const int b0 = min((int)threadIdx.x * per, p.B), b1 = min(b0 + per, p.B);
@@ -179,13 +198,14 @@ __global__ void __launch_bounds__(kWarps * 32) part_kernel(const AttnDev p) {
   int *sum = reinterpret_cast<int *>(sm + smem_tiles<D>());
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const uint32_t sm0 = smem_addr(sm);
-  pdl_wait();
+  // Behind the tensor-core kernel this one starts as blocks of that one end;
+  // it reads nothing of its, and only waits for it before it ends itself.
+  if (!p.tc_rows) pdl_wait();
   pdl_trigger();
   const Line line = make_line(p, gridDim.x, sum, red);
   const long long c = blockIdx.x;
-  if (c >= line.N) return;
-  long long t0 = c * line.total / line.N;
-  const long long t_end = (c + 1) * line.total / line.N;
+  long long t0 = c < line.N ? c * line.total / line.N : 0;
+  const long long t_end = c < line.N ? (c + 1) * line.total / line.N : 0;
 
   while (t0 < t_end) {
     // ---- which item, and which of its tiles
@@ -221,8 +241,8 @@ __global__ void __launch_bounds__(kWarps * 32) part_kernel(const AttnDev p) {
       kv = k / p.own_tiles;
       row0 = k % p.own_tiles * kRows;
       n_rows = min(kRows, p.T * p.G - row0);
-      lo = line.prefix;
-      hi = line.prefix + own_len(p, b, line.prefix);
+      lo = own_start(p, b, line.prefix);
+      hi = lo + own_len(p, b, line.prefix);
     }
     const int first = (int)(t0 - item_t0), n_tiles = (int)(min(t_end, item_t1) - t0);
     t0 += n_tiles;
@@ -244,7 +264,8 @@ __global__ void __launch_bounds__(kWarps * 32) part_kernel(const AttnDev p) {
       if (r < n_rows) {
         int rb, rt, rh;
         row_of(r, rb, rt, rh);
-        sees[h] = max(0, max(seq_len(p, rb), 0) - (p.T - 1 - rt));
+        // (a row that does not see all of the prefix does not take this part)
+        sees[h] = b < 0 ? hi : max(0, max(seq_len(p, rb), 0) - (p.T - 1 - rt));
         qp = p.q + rb * p.q_bs + rt * p.q_ts + rh * p.q_hs;
         min_sees = min(min_sees, sees[h]);
       }
@@ -256,7 +277,7 @@ __global__ void __launch_bounds__(kWarps * 32) part_kernel(const AttnDev p) {
     }
     min_sees = __reduce_min_sync(0xffffffffu, min_sees);
 
-    const int *list = b >= 0 ? p.table + (long long)b * p.table_width : p.prefix_pages;
+    const int *table = p.table + (long long)b * p.table_width;  // (not used by prefix items)
     auto load_tile = [&](int i) {  // tile first + i into stage i % kStages
       const uint32_t dst = sm0 + (i % kStages) * 2 * tile_bytes<D>();
       const int pos0 = lo + (first + i) * kKeys;
@@ -268,7 +289,7 @@ __global__ void __launch_bounds__(kWarps * 32) part_kernel(const AttnDev p) {
         long long off = 0;
         if (live) {
           const int pi = pos / p.page;
-          int pg = list[pi];
+          int pg = pos < line.prefix ? p.prefix_pages[pi] : table[pi];
           if ((unsigned)pg >= (unsigned)p.n_pages) {
             report(p.status, MK_ERR_DEVICE_INPUT);
             pg = 0;
@@ -438,48 +459,612 @@ __global__ void __launch_bounds__(kWarps * 32) part_kernel(const AttnDev p) {
     }
     __syncthreads();  // before the next item's tiles
   }
+  if (p.tc_rows) pdl_wait();
 }
 
-// Join the partials of every row: a warp per row.
+// ---------------------------------------------------------------- the prefix on the tensor cores
+//
+// S = Q K^T and O += P V as 128 x 128 matrix instructions (tcgen05, operands in
+// shared memory, accumulators in tensor memory).  A block has two halves of
+// four softmax warps, a row per thread, each half with its own S, O, m and l:
+//   tc_rows = 256: the halves take 128 rows each and read the same K/V tiles;
+//   tc_rows = 128: both take the same rows, and every other K/V tile.
+// One half's softmax thus runs while the tensor cores work for the other.
+// Four warps copy the K/V tiles (16 bytes a time, rows from the page list) into
+// a ring in the order they are needed, and one thread issues the matrix
+// instructions.
+// P takes S's place in tensor memory, rounded to the operands' type: half a
+// step (2^-8 or 2^-11) of each weight, as the output's own rounding.
+// A row's maximum only moves when it grows by more than 2^8: until then the
+// weights are at most 2^8, which neither type nor the 32-bit sums mind, and O
+// need not be rescaled.
+
+constexpr int kTcRows = 128;  // rows of a half
+constexpr int kTcKeys = 128;  // positions of a tile
+constexpr int kTcThreads = 13 * 32;  // warps 0-3 and 4-7: softmax; 8-11: copies; 12: matrix instructions
+constexpr int kTcLag = 2;     // copies of a tile stay in flight behind this many later ones
+constexpr float kTcGrow = 8.f;
+template <int D>
+constexpr int tc_tile() {
+  return kTcKeys * D * 2;
+}
+template <int D>
+constexpr int tc_ring() {
+  return D == 128 ? 5 : 10;  // tiles of K or V in flight or in use: 160 KB
+}
+template <int D>
+constexpr int tc_smem() {
+  return (2 + tc_ring<D>()) * tc_tile<D>() + 1024;
+}
+
+// Byte of element chunk c (8 elements) of row r in a tile of 128 rows: 64
+// elements (128 bytes) of every row, then the next 64; the eight chunks of 128
+// bytes exchanged by the row number (the 128-byte swizzle of the operand
+// descriptors).
+__device__ __forceinline__ uint32_t tc_at(int r, int c) {
+  return (uint32_t)((c >> 3) * (kTcKeys * 128) + r * 128 + (((c & 7) ^ (r & 7)) << 4));
+}
+// Operand descriptor: 128-byte swizzle, 8-row groups 1024 bytes apart; lbo: from
+// 64 elements of the leading dimension to the next 64 (read for V only).
+__device__ __forceinline__ uint64_t tc_desc(uint32_t addr, uint32_t lbo) {
+  return (uint64_t)((addr >> 4) & 0x3FFFu) | ((uint64_t)((lbo >> 4) & 0x3FFFu) << 16) | ((uint64_t)(1024 >> 4) << 32) |
+         (1ull << 46) | (2ull << 61);
+}
+__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool add) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}\n" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc), "r"((uint32_t)add)
+      : "memory");
+}
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, bool add) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}\n" ::"r"(d),
+      "r"(a), "l"(b), "r"(idesc), "r"((uint32_t)add)
+      : "memory");
+}
+__device__ __forceinline__ void mma_commit(uint64_t *bar) {
+  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_addr(bar))
+               : "memory");
+}
+__device__ __forceinline__ void tc_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void tc_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void tm_ld32(uint32_t a, uint32_t (&r)[32]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,"
+      "%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
+        "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
+        "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+      : "r"(a)
+      : "memory");
+}
+__device__ __forceinline__ void tm_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
+__device__ __forceinline__ void tm_st16(uint32_t a, const uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(a),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+      : "memory");
+}
+__device__ __forceinline__ void tm_st32(uint32_t a, const uint32_t (&r)[32]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,"
+      "%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(a),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]),
+      "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]),
+      "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
+      : "memory");
+}
+__device__ __forceinline__ void tm_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+__device__ __forceinline__ void fence_smem_async() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
+__device__ __forceinline__ void bar_init(uint64_t *b, uint32_t n) {
+  asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(smem_addr(b)), "r"(n) : "memory");
+}
+__device__ __forceinline__ void bar_arrive(uint64_t *b) {
+  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_addr(b)) : "memory");
+}
+__device__ __forceinline__ bool bar_try(uint64_t *b, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n selp.u32 %0, 1, 0, p;\n}\n"
+      : "=r"(ok)
+      : "r"(smem_addr(b)), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
+
+struct TcShared {
+  uint64_t full[16], empty[16];  // ring entries
+  uint64_t q_full[2], s_full[2], p_full[2], o_full[2], drain;
+  uint32_t tmem;
+  volatile int dead;  // a wait gave up
+};
+
+// Wait for a phase; false when it does not come within a second (or another
+// wait has given up): every role then runs to the kernel's end.
+__device__ bool bar_wait(TcShared *sh, uint64_t *b, uint32_t parity, int32_t *status) {
+  if (bar_try(b, parity)) return true;
+  uint64_t t0, t;
+  asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t0));
+  while (!bar_try(b, parity)) {
+    asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t));
+    if (sh->dead || t - t0 > 1000000000ull) {
+      sh->dead = 1;
+      report(status, MK_ERR_TIMEOUT);
+      return false;
+    }
+  }
+  return true;
+}
+
+// The blocks' line of tiles, as for the other items.
+struct TcLine {
+  int prefix, tiles, n_items;
+  long long total, N;
+};
+__device__ __forceinline__ TcLine tc_line(const AttnDev &p, int prefix, int blocks) {
+  TcLine l;
+  l.prefix = prefix;
+  l.tiles = (prefix + kTcKeys - 1) / kTcKeys;
+  l.n_items = p.nkv * p.tc_groups;
+  l.total = (long long)l.tiles * l.n_items;
+  l.N = min((long long)blocks, l.total);
+  return l;
+}
+
 template <class T, int D>
-__global__ void __launch_bounds__(128) join_kernel(const AttnDev p, int N) {
+__global__ void __launch_bounds__(kTcThreads, 1) tc_kernel(const AttnDev p) {
+  extern __shared__ char sm_raw[];
+  __shared__ TcShared sh;
+  constexpr int kRing = tc_ring<D>();
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const uint32_t base = (smem_addr(sm_raw) + 1023) & ~1023u;
+  char *sm = sm_raw + (base - smem_addr(sm_raw));
+  const uint32_t ring = base + 2 * tc_tile<D>();
+  if (tid == 0) {
+    for (int i = 0; i < kRing; ++i) {
+      bar_init(&sh.full[i], 4);
+      bar_init(&sh.empty[i], 1);
+    }
+    for (int w = 0; w < 2; ++w) {
+      bar_init(&sh.q_full[w], 4);
+      bar_init(&sh.s_full[w], 1);
+      bar_init(&sh.p_full[w], 4);
+      bar_init(&sh.o_full[w], 1);
+    }
+    bar_init(&sh.drain, 1);
+    sh.dead = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  if (warp == 12)
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_addr(&sh.tmem)) : "memory");
+  pdl_wait();
+  pdl_trigger();
+  tc_before();
+  __syncthreads();
+  tc_after();
+  const uint32_t tm = sh.tmem;
+  const TcLine line = tc_line(p, prefix_of(p), gridDim.x);
+  const long long c = blockIdx.x;
+  const bool pair = p.tc_rows == 2 * kTcRows;  // the halves have rows of their own
+  const int dist = pair ? 1 : 2;               // K tiles that are multiplied ahead of their V
+  const int R = p.B * p.T * p.G;
+  const long long t_begin = c < line.N ? c * line.total / line.N : 0, t_end = c < line.N ? (c + 1) * line.total / line.N : 0;
+  auto s_of = [&](int w) { return tm + w * 128; };
+  auto o_of = [&](int w) { return tm + 256 + w * D; };
+
+  if (warp >= 8 && warp < 12) {
+    // ---------------- copies
+    int g = 0, told = 0;  // ring entries begun; of which announced
+    bool ok = true;
+    const int t = tid - 256;
+    auto tell = [&](int upto) {  // this warp's part of the entries before `upto` has landed
+      fence_smem_async();
+      __syncwarp();
+      if (lane == 0)
+        for (int i = told; i < upto; ++i) bar_arrive(&sh.full[i % kRing]);
+      told = max(told, upto);
+    };
+    for (long long t0 = t_begin; ok && t0 < t_end;) {
+      const int item = (int)(t0 / line.tiles), first = (int)(t0 % line.tiles);
+      const int n = (int)min(t_end - t0, (long long)(line.tiles - first)), kv = item / p.tc_groups;
+      t0 += n;
+      auto put = [&](const char *src, int j) {
+        const int slot = g % kRing;
+        if (!ok) return;
+        const uint32_t phase = ((g / kRing) & 1) ^ 1;
+        if (g >= kRing && !__all_sync(0xffffffffu, bar_try(&sh.empty[slot], phase))) {
+          cp_wait<0>();  // nothing is held back while this warp waits
+          tell(g);
+          ok = __all_sync(0xffffffffu, bar_wait(&sh, &sh.empty[slot], phase, p.status));
+          if (!ok) return;
+        }
+        const uint32_t dst = ring + slot * tc_tile<D>();
+        constexpr int kChunks = D / 8, kPass = 128 / kChunks;
+        const int ch = t % kChunks, pos0 = (first + j) * kTcKeys + t / kChunks;
+        const char *from = src + kv * p.kv_hs + ch * 16;
+#pragma unroll 4
+        for (int x = 0; x < kTcKeys / kPass; ++x) {
+          const int pos = pos0 + x * kPass;
+          const bool live = pos < line.prefix;
+          long long off = 0;
+          if (live) {
+            const int pi = pos / p.page;
+            int pg = p.prefix_pages[pi];
+            if ((unsigned)pg >= (unsigned)p.n_pages) {
+              report(p.status, MK_ERR_DEVICE_INPUT);
+              pg = 0;
+            }
+            off = (long long)pg * p.kv_ps + (pos - pi * p.page) * p.kv_rs;
+          }
+          cp16(dst + tc_at(x * kPass + t / kChunks, ch), from + off, live);
+        }
+        cp_commit();
+        ++g;
+        if (g - told > kTcLag) {
+          cp_wait<kTcLag>();
+          tell(g - kTcLag);
+        }
+      };
+      for (int j = 0; j < min(dist, n); ++j) put(p.k, j);
+      for (int j = 0; j < n; ++j) {
+        put(p.v, j);
+        if (j + dist < n) put(p.k, j + dist);
+      }
+    }
+    cp_wait<0>();
+    tell(g);
+  } else if (warp == 12) {
+    // ---------------- matrix instructions
+    if (lane == 0) {
+      constexpr uint32_t kType = sizeof(T) == 2 && std::is_same<T, __nv_bfloat16>::value ? 1u : 0u;
+      // 32-bit accumulators, both operands of this type, 128 rows; N = 128 positions, or N = D with V's
+      // leading dimension the other way round
+      constexpr uint32_t kS = (1u << 4) | (kType << 7) | (kType << 10) | ((128u / 8) << 17) | ((128u / 16) << 24);
+      constexpr uint32_t kO = (1u << 4) | (kType << 7) | (kType << 10) | (1u << 16) | ((uint32_t)(D / 8) << 17) | ((128u / 16) << 24);
+      int g = 0;                       // ring entries used
+      uint32_t q_phase[2] = {0, 0}, p_phase[2] = {0, 0};
+      bool ok = true;
+      auto take = [&]() {  // the next ring entry's tile
+        const int slot = g % kRing;
+        ok = ok && bar_wait(&sh, &sh.full[slot], (g / kRing) & 1, p.status);
+        ++g;
+        return slot;
+      };
+      for (long long t0 = t_begin; ok && t0 < t_end;) {
+        const int item = (int)(t0 / line.tiles), first = (int)(t0 % line.tiles);
+        const int n = (int)min(t_end - t0, (long long)(line.tiles - first));
+        t0 += n;
+        const int row0 = item % p.tc_groups * p.tc_rows;
+        const bool two = pair && row0 + kTcRows < R;  // the second half has rows
+        for (int w = 0; w < 2; ++w)  // the halves that have tiles here
+          if (w == 0 || (pair ? two : n > 1)) {
+            ok = ok && bar_wait(&sh, &sh.q_full[w], q_phase[w], p.status);
+            q_phase[w] ^= 1;
+          }
+        if (!ok) break;
+        auto scores = [&](int w, int slot) {
+          const uint32_t q = base + w * tc_tile<D>(), k = ring + slot * tc_tile<D>();
+#pragma unroll
+          for (int i = 0; i < D / 16; ++i) {
+            const uint32_t o = (i / 4) * (kTcKeys * 128) + (i % 4) * 32;
+            mma_ss(s_of(w), tc_desc(q + o, 16), tc_desc(k + o, 16), kS, i > 0);
+          }
+          mma_commit(&sh.s_full[w]);
+        };
+        auto values = [&](int w, int slot, bool add) {
+          const uint32_t v = ring + slot * tc_tile<D>();
+#pragma unroll
+          for (int i = 0; i < kTcKeys / 16; ++i)
+            mma_ts(o_of(w), s_of(w) + i * 8, tc_desc(v + i * 2048, kTcKeys * 128), kO, add || i > 0);
+        };
+        auto weights = [&](int w) {  // half w has put P in S's place
+          ok = ok && bar_wait(&sh, &sh.p_full[w], p_phase[w], p.status);
+          p_phase[w] ^= 1;
+          tc_after();
+        };
+        if (pair) {
+          int k = take();
+          if (!ok) break;
+          scores(0, k);
+          if (two) scores(1, k);
+          mma_commit(&sh.empty[k]);
+          for (int j = 0; ok && j < n; ++j) {
+            const int v = take();
+            weights(0);
+            if (!ok) break;
+            values(0, v, j > 0);
+            if (j + 1 < n) {
+              k = take();
+              if (!ok) break;
+              scores(0, k);
+            } else {
+              mma_commit(&sh.o_full[0]);
+            }
+            if (two) {
+              weights(1);
+              if (!ok) break;
+              values(1, v, j > 0);
+            }
+            mma_commit(&sh.empty[v]);
+            if (j + 1 < n) {
+              if (two) scores(1, k);
+              mma_commit(&sh.empty[k]);
+            } else if (two) {
+              mma_commit(&sh.o_full[1]);
+            }
+          }
+        } else {
+          for (int j = 0; j < min(2, n); ++j) {
+            const int k = take();
+            if (!ok) break;
+            scores(j, k);
+            mma_commit(&sh.empty[k]);
+          }
+          for (int j = 0; ok && j < n; ++j) {
+            const int v = take();
+            weights(j & 1);
+            if (!ok) break;
+            values(j & 1, v, j > 1);
+            mma_commit(&sh.empty[v]);
+            if (j + 2 < n) {
+              const int k = take();
+              if (!ok) break;
+              scores(j & 1, k);
+              mma_commit(&sh.empty[k]);
+            } else {
+              mma_commit(&sh.o_full[j & 1]);
+            }
+          }
+        }
+      }
+      if (!ok) {  // given up: the instructions in flight end before tensor memory goes
+        mma_commit(&sh.drain);
+        for (int i = 0; i < 100000 && !bar_try(&sh.drain, 0); ++i) {
+        }
+      }
+    }
+    __syncwarp();
+  } else if (warp < 8) {
+    // ---------------- softmax: row r of half w
+    const int w = warp >> 2, r = (warp & 3) * 32 + lane;
+    const uint32_t lanes = (uint32_t)(warp & 3) << 21;  // this warp's 32 lanes of tensor memory
+    uint32_t s_phase = 0, o_phase = 0;
+    bool ok = true;
+    for (long long t0 = t_begin; ok && t0 < t_end;) {
+      const int item = (int)(t0 / line.tiles), first = (int)(t0 % line.tiles);
+      const int n = (int)min(t_end - t0, (long long)(line.tiles - first)), kv = item / p.tc_groups;
+      t0 += n;
+      const int row = item % p.tc_groups * p.tc_rows + (pair ? w * kTcRows : 0) + r;
+      const bool live = row < R, any_live = row - lane < R, half_live = row - r < R;
+      float m = -INFINITY, l = 0.f;
+      const int step = pair ? 1 : 2, j0 = pair ? 0 : w;
+      const bool some = half_live && j0 < n;  // this half has tiles
+      if (some) {
+        // this row of Q (the S of the last item is done with the old one)
+        const char *qp = nullptr;
+        if (live) {
+          const int rh = kv * p.G + row % p.G, rt = row / p.G % p.T, rb = row / p.G / p.T;
+          qp = p.q + rb * p.q_bs + rt * p.q_ts + rh * p.q_hs;
+        }
+#pragma unroll
+        for (int i = 0; i < D / 8; ++i) {
+          uint4 x = make_uint4(0, 0, 0, 0);
+          if (live) {
+            x = *reinterpret_cast<const uint4 *>(qp + i * 16);
+            x.x ^= p.flip;
+            x.y ^= p.flip;
+            x.z ^= p.flip;
+            x.w ^= p.flip;
+          }
+          *reinterpret_cast<uint4 *>(sm + w * tc_tile<D>() + tc_at(r, i)) = x;
+        }
+        fence_smem_async();
+        __syncwarp();
+        if (lane == 0) bar_arrive(&sh.q_full[w]);
+      }
+      for (int j = j0; some && j < n; j += step) {
+        ok = bar_wait(&sh, &sh.s_full[w], s_phase, p.status);
+        ok = __all_sync(0xffffffffu, ok);
+        s_phase ^= 1;
+        if (!ok) break;
+        tc_after();
+        if (any_live) {
+          const int valid = min(kTcKeys, line.prefix - (first + j) * kTcKeys);
+          const uint32_t s = s_of(w) + lanes;
+          uint32_t x[32];
+          float top = -INFINITY;
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            tm_ld32(s + q * 32, x);
+            tm_wait_ld();
+            if (valid >= kTcKeys) {
+#pragma unroll
+              for (int i = 0; i < 32; ++i) top = fmaxf(top, __uint_as_float(x[i]));
+            } else {
+#pragma unroll
+              for (int i = 0; i < 32; ++i) top = q * 32 + i < valid ? fmaxf(top, __uint_as_float(x[i])) : top;
+            }
+          }
+          top = top == -INFINITY ? top : top * p.scale2;
+          if (j == j0) {
+            m = top;
+          } else {
+            const bool grow = top > m + kTcGrow;
+            if (__any_sync(0xffffffffu, grow)) {
+              // (the last P V is complete: S came after it)
+              const float f = grow ? exp2_(m - top) : 1.f;
+              if (grow) m = top;
+              l *= f;
+              for (int q = 0; q < D / 32; ++q) {
+                tm_ld32(o_of(w) + lanes + q * 32, x);
+                tm_wait_ld();
+#pragma unroll
+                for (int i = 0; i < 32; ++i) x[i] = __float_as_uint(__uint_as_float(x[i]) * f);
+                tm_st32(o_of(w) + lanes + q * 32, x);
+              }
+            }
+          }
+          const float b = m == -INFINITY ? 0.f : m;
+          float sum0 = 0.f, sum1 = 0.f;
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            tm_ld32(s + q * 32, x);
+            tm_wait_ld();
+            uint32_t h[16];
+#pragma unroll
+            for (int i = 0; i < 32; i += 2) {
+              float a0 = __uint_as_float(x[i]), a1 = __uint_as_float(x[i + 1]);
+              if (valid < kTcKeys) {
+                a0 = q * 32 + i < valid ? a0 : -INFINITY;
+                a1 = q * 32 + i + 1 < valid ? a1 : -INFINITY;
+              }
+              const float e0 = a0 == -INFINITY ? 0.f : exp2_(fmaf(a0, p.scale2, -b));
+              const float e1 = a1 == -INFINITY ? 0.f : exp2_(fmaf(a1, p.scale2, -b));
+              sum0 += e0;
+              sum1 += e1;
+              h[i / 2] = Num<T>::pack(e0, e1);
+            }
+            tm_st16(s + q * 16, h);
+          }
+          l += sum0 + sum1;
+          tm_wait_st();
+        }
+        tc_before();
+        __syncwarp();
+        if (lane == 0) bar_arrive(&sh.p_full[w]);
+      }
+      if (!ok) break;
+      // ---- the partial result
+      if (some) {
+        ok = bar_wait(&sh, &sh.o_full[w], o_phase, p.status);
+        ok = __all_sync(0xffffffffu, ok);
+        o_phase ^= 1;
+        if (!ok) break;
+        tc_after();
+      }
+      if (any_live) {
+        const long long slot = (c + item) * 2 + w;
+        if (some)
+          for (int q = 0; q < D / 32; ++q) {
+            uint32_t x[32];
+            tm_ld32(o_of(w) + lanes + q * 32, x);
+            tm_wait_ld();
+            if (live)
+#pragma unroll
+              for (int i = 0; i < 8; ++i)
+                p.tc_o[(slot * (D / 4) + q * 8 + i) * kTcRows + r] =
+                    make_float4(__uint_as_float(x[4 * i]), __uint_as_float(x[4 * i + 1]), __uint_as_float(x[4 * i + 2]),
+                                __uint_as_float(x[4 * i + 3]));
+          }
+        if (live) p.tc_ml[slot * kTcRows + r] = make_float2(m, l);
+      }
+      tc_before();
+    }
+  }
+  __syncthreads();
+  if (warp == 12) {
+    tc_after();
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tm) : "memory");
+  }
+}
+
+// Join the partials of every row: a warp per row.  The lanes look at the
+// partials' maxima and sums, a partial each; then each lane adds up four
+// elements (D = 64: each half of the warp every other partial).
+template <class T, int D>
+__global__ void __launch_bounds__(128) join_kernel(const AttnDev p, int N, int tc_n) {
   extern __shared__ int sum[];
   __shared__ int red[4];
   const int lane = threadIdx.x & 31;
   pdl_wait();
   const Line line = make_line(p, N, sum, red);
+  const TcLine tc = tc_line(p, p.tc_rows ? line.prefix : 0, tc_n);
   const int rows = p.B * p.T * p.nq;
   for (int x = blockIdx.x * 4 + (threadIdx.x >> 5); x < rows; x += gridDim.x * 4) {
     const int h = x % p.nq, t = x / p.nq % p.T, b = x / p.nq / p.T;
     if (p.lens[b] < 0) continue;
-    const int kv = h / p.G, g = h % p.G;
-    float M = -INFINITY, L = 0.f, o[D / 32] = {};
-    auto add = [&](int item, long long t0, long long t1, int r) {
-      if (t1 <= t0) return;
-      // the block that owns tile t is the largest c with c * total / N <= t;
-      // with N <= total every block between the two has a part of this item
-      const long long c0 = ((t0 + 1) * line.N - 1) / line.total, c1 = (t1 * line.N - 1) / line.total;
-      for (long long s = c0 + item; s <= c1 + item; ++s) {
-        const float2 ml = p.part_ml[s * kRows + r];
-        const float mn = fmaxf(M, ml.x), base = mn == -INFINITY ? 0.f : mn;
-        const float f0 = exp2_(M - base), f1 = exp2_(ml.x - base);
-        M = mn;
-        L = L * f0 + ml.y * f1;
-        const float *a = p.part_o + (s * kRows + r) * D + lane * (D / 32);
-#pragma unroll
-        for (int i = 0; i < D / 32; ++i) o[i] = o[i] * f0 + a[i] * f1;
-      }
+    const int kv = h / p.G, g = h % p.G, pr = (b * p.T + t) * p.G + g;
+    // partials of this row: n_tc of the tensor cores, then n_pre and n_own of the other kernel
+    int n_tc = 0, n_pre = 0, n_own = 0, r_tc = 0, r_own = 0;
+    long long s_tc = 0, s_pre = 0, s_own = 0;
+    // the block that owns tile t is the largest c with c * total / N <= t; with
+    // N <= total every block between two that share an item has a part of it
+    auto span = [](long long t0, long long t1, long long n, long long total, long long item, long long &first) {
+      first = ((t0 + 1) * n - 1) / total + item;
+      return (int)((t1 * n - 1) / total + item - first) + 1;
     };
-    const int tiles = p.n_prefix_items / p.nkv, pr = (b * p.T + t) * p.G + g;
-    const int ip = kv * tiles + pr / kRows;
-    add(ip, (long long)ip * line.prefix_tiles, (long long)(ip + 1) * line.prefix_tiles, pr % kRows);
-    const int per = p.nkv * p.own_tiles, nt = sum[b + 1] - sum[b], w = t * p.G + g, k = kv * p.own_tiles + w / kRows;
-    const long long base = line.own0 + (long long)sum[b] * per + (long long)k * nt;
-    add(p.n_prefix_items + b * per + k, base, base + nt, w % kRows);
-    const float inv = L > 0.f ? 1.f / L : L == 0.f ? 0.f : L;  // a NaN stays
-    uint32_t *op = reinterpret_cast<uint32_t *>(p.out + b * p.o_bs + t * p.o_ts + h * p.o_hs + lane * (D / 32) * 2);
+    if (shares(p, b, line.prefix)) {
+      if (p.tc_rows) {
+        const long long item = kv * p.tc_groups + pr / p.tc_rows;
+        n_tc = span(item * tc.tiles, (item + 1) * tc.tiles, tc.N, tc.total, item, s_tc);
+        r_tc = pr % p.tc_rows;
+        if (p.tc_rows == kTcRows) n_tc *= 2;  // both halves hold a part of the row
+      } else {
+        const int item = kv * (p.n_prefix_items / p.nkv) + pr / kRows;
+        n_pre = span((long long)item * line.prefix_tiles, (long long)(item + 1) * line.prefix_tiles, line.N, line.total, item, s_pre);
+      }
+    }
+    const int nt = sum[b + 1] - sum[b];
+    if (nt > 0) {
+      const int per = p.nkv * p.own_tiles, w = t * p.G + g, k = kv * p.own_tiles + w / kRows;
+      const long long t0 = line.own0 + (long long)sum[b] * per + (long long)k * nt;
+      n_own = span(t0, t0 + nt, line.N, line.total, p.n_prefix_items + b * per + k, s_own);
+      r_own = w % kRows;
+    }
+    const int n = n_tc + n_pre + n_own;
+    auto tc_slot = [&](int i) {  // half-slot of the i-th
+      return p.tc_rows == kTcRows ? s_tc * 2 + i : (s_tc + i) * 2 + r_tc / kTcRows;
+    };
+    auto part_row = [&](int i) {
+      i -= n_tc;
+      return i < n_pre ? (s_pre + i) * kRows + pr % kRows : (s_own + i - n_pre) * kRows + r_own;
+    };
+    auto ml_of = [&](int i) { return i < n_tc ? p.tc_ml[tc_slot(i) * kTcRows + r_tc % kTcRows] : p.part_ml[part_row(i)]; };
+    float M = -INFINITY, L = 0.f;
+    for (int i = lane; i < n; i += 32) {
+      const float2 ml = ml_of(i);
+      if (ml.y != 0.f) M = fmaxf(M, ml.x);
+    }
 #pragma unroll
-    for (int i = 0; i < D / 64; ++i) op[i] = Num<T>::pack(L == 0.f ? 0.f : o[2 * i] * inv, L == 0.f ? 0.f : o[2 * i + 1] * inv);
+    for (int o = 16; o; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+    const float base = M == -INFINITY ? 0.f : M;
+    for (int i = lane; i < n; i += 32) {
+      const float2 ml = ml_of(i);
+      if (ml.y != 0.f) L += ml.y * exp2_(ml.x - base);
+    }
+#pragma unroll
+    for (int o = 16; o; o >>= 1) L += __shfl_xor_sync(0xffffffffu, L, o);
+    constexpr int kWays = 128 / D;
+    const int d4 = lane % (D / 4);
+    float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+    for (int i = lane / (D / 4); i < n; i += kWays) {
+      const float2 ml = ml_of(i);
+      if (ml.y == 0.f) continue;  // nothing there (its o was not written)
+      const float f = exp2_(ml.x - base);
+      const float4 y = i < n_tc ? p.tc_o[(tc_slot(i) * (D / 4) + d4) * kTcRows + r_tc % kTcRows]
+                                : *reinterpret_cast<const float4 *>(p.part_o + part_row(i) * D + d4 * 4);
+      a.x += f * y.x;
+      a.y += f * y.y;
+      a.z += f * y.z;
+      a.w += f * y.w;
+    }
+    if (kWays == 2) {
+      a.x += __shfl_xor_sync(0xffffffffu, a.x, 16);
+      a.y += __shfl_xor_sync(0xffffffffu, a.y, 16);
+      a.z += __shfl_xor_sync(0xffffffffu, a.z, 16);
+      a.w += __shfl_xor_sync(0xffffffffu, a.w, 16);
+    }
+    const float inv = L == 0.f ? 0.f : 1.f / L;  // (a NaN stays)
+    if (lane < D / 4)
+      *reinterpret_cast<uint2 *>(p.out + b * p.o_bs + t * p.o_ts + h * p.o_hs + d4 * 8) =
+          make_uint2(Num<T>::pack(a.x * inv, a.y * inv), Num<T>::pack(a.z * inv, a.w * inv));
     if (p.lse && lane == 0) p.lse[x] = L == 0.f ? -INFINITY : (M + log2f(L)) * 0.6931471805599453f;
   }
 }
@@ -499,8 +1084,8 @@ int check(const mk_attn_shared_args *a) {
   return MK_OK;
 }
 
-// Blocks of the partial kernel on this device: as many as fit at once.
-constexpr int kBlocksPerSm = 2;
+constexpr int kBlocksPerSm = 2;  // of the partial kernel, as many as fit at once
+constexpr int kTcMinRows = 17;   // rows of a K/V head from which the prefix goes to the tensor cores' kernel
 
 void fill(const mk_attn_shared_args *a, AttnDev *d) {
   d->B = a->batch;
@@ -508,29 +1093,47 @@ void fill(const mk_attn_shared_args *a, AttnDev *d) {
   d->nq = a->n_q_heads;
   d->nkv = a->n_kv_heads;
   d->G = d->nq / d->nkv;
-  d->n_prefix_items = a->n_prefix_pages > 0 ? d->nkv * ((d->B * d->T * d->G + kRows - 1) / kRows) : 0;
+  const int R = d->B * d->T * d->G;
+  d->tc_rows = a->n_prefix_pages > 0 && R >= kTcMinRows ? (R <= kTcRows ? kTcRows : 2 * kTcRows) : 0;
+  d->tc_groups = d->tc_rows ? (R + d->tc_rows - 1) / d->tc_rows : 0;
+  d->n_prefix_items = a->n_prefix_pages > 0 && !d->tc_rows ? d->nkv * ((R + kRows - 1) / kRows) : 0;
   d->own_tiles = (d->T * d->G + kRows - 1) / kRows;
   d->n_items = d->n_prefix_items + d->B * d->nkv * d->own_tiles;
 }
 
-int grid_of(int *out) {
-  int dev = 0, sms = 0;
+int sm_count(int *out) {
+  int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
-  if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
-  *out = sms * kBlocksPerSm;
+  if (e == cudaSuccess) e = cudaDeviceGetAttribute(out, cudaDevAttrMultiProcessorCount, dev);
   return serve_code(e);
 }
 
+// The parts of the workspace: bytes of each, in order.
+struct Sizes {
+  int64_t part_o, part_ml, tc_o, tc_ml;
+};
+Sizes sizes_of(const AttnDev &d, int head_dim, int sms) {
+  const int64_t rows = ((int64_t)sms * kBlocksPerSm + d.n_items) * kRows;
+  const int64_t tc = d.tc_rows ? ((int64_t)sms + d.nkv * d.tc_groups) * 2 * kTcRows : 0;
+  return Sizes{rows * head_dim * 4, rows * 8, tc * head_dim * 4, tc * 8};
+}
+
 template <class T, int D>
-int launch(const AttnDev &p, int N, cudaStream_t st) {
+int launch(const AttnDev &p, int sms, cudaStream_t st) {
   const size_t smem = smem_tiles<D>() + sizeof(int) * (p.B + 1);
+  const int N = sms * kBlocksPerSm;
   static_assert(kStages * 2 * kKeys >= kWarps * kRows * 2, "the warps' partials fit into the tiles");
-  int rc = serve_code(cudaFuncSetAttribute((const void *)part_kernel<T, D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                           (int)smem));
-  if (!rc) rc = serve_launch(part_kernel<T, D>, dim3(N), kWarps * 32, smem, st, false, 1, p);
+  int rc = MK_OK;
+  if (p.tc_rows) {
+    rc = serve_code(cudaFuncSetAttribute((const void *)tc_kernel<T, D>, cudaFuncAttributeMaxDynamicSharedMemorySize, tc_smem<D>()));
+    if (!rc) rc = serve_launch(tc_kernel<T, D>, dim3(sms), kTcThreads, tc_smem<D>(), st, false, 1, p);
+  }
+  if (!rc)
+    rc = serve_code(cudaFuncSetAttribute((const void *)part_kernel<T, D>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem));
+  if (!rc) rc = serve_launch(part_kernel<T, D>, dim3(N), kWarps * 32, smem, st, p.tc_rows > 0, 1, p);
   if (rc) return rc;
-  const int rows = p.B * p.T * p.nq, grid = std::min((rows + 3) / 4, N * 4);
-  return serve_launch(join_kernel<T, D>, dim3(grid), 128, sizeof(int) * (p.B + 1), st, true, 1, p, N);
+  const int rows = p.B * p.T * p.nq, grid = std::min((rows + 3) / 4, sms * 16);
+  return serve_launch(join_kernel<T, D>, dim3(grid), 128, sizeof(int) * (p.B + 1), st, true, 1, p, N, sms);
 }
 
 }  // namespace
@@ -542,9 +1145,10 @@ extern "C" int64_t mk_attn_shared_workspace_bytes(const mk_attn_shared_args *a) 
   if (check(a)) return 0;
   AttnDev d;
   fill(a, &d);
-  int N = 0;
-  if (grid_of(&N)) return 0;
-  return ((int64_t)N + d.n_items) * kRows * (a->head_dim * 4 + 8) + 256;
+  int sms = 0;
+  if (sm_count(&sms)) return 0;
+  const Sizes z = sizes_of(d, a->head_dim, sms);
+  return z.part_o + z.part_ml + z.tc_o + z.tc_ml;
 }
 
 extern "C" int mk_attn_shared(const mk_attn_shared_args *a, void *workspace, void *stream) {
@@ -587,13 +1191,16 @@ extern "C" int mk_attn_shared(const mk_attn_shared_args *a, void *workspace, voi
   d.table_width = a->table_width;
   d.scale2 = (float)(std::fabs((double)a->scale) * 1.4426950408889634);
   d.flip = a->scale < 0.f ? 0x80008000u : 0u;
-  int N = 0;
-  if ((rc = grid_of(&N))) return rc;
-  const int64_t slots = (int64_t)N + d.n_items;
-  d.part_o = (float *)workspace;
-  d.part_ml = (float2 *)((char *)workspace + slots * kRows * a->head_dim * 4);
+  int sms = 0;
+  if ((rc = sm_count(&sms))) return rc;
+  const Sizes z = sizes_of(d, a->head_dim, sms);
+  char *w = (char *)workspace;
+  d.part_o = (float *)w;
+  d.tc_o = (float4 *)(w + z.part_o);
+  d.part_ml = (float2 *)(w + z.part_o + z.tc_o);
+  d.tc_ml = (float2 *)(w + z.part_o + z.tc_o + z.part_ml);
   cudaStream_t st = (cudaStream_t)stream;
   if (a->dtype == MK_DTYPE_BF16)
-    return a->head_dim == 64 ? launch<__nv_bfloat16, 64>(d, N, st) : launch<__nv_bfloat16, 128>(d, N, st);
-  return a->head_dim == 64 ? launch<__half, 64>(d, N, st) : launch<__half, 128>(d, N, st);
+    return a->head_dim == 64 ? launch<__nv_bfloat16, 64>(d, sms, st) : launch<__nv_bfloat16, 128>(d, sms, st);
+  return a->head_dim == 64 ? launch<__half, 64>(d, sms, st) : launch<__half, 128>(d, sms, st);
 }

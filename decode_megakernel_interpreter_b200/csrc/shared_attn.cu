@@ -26,6 +26,7 @@ constexpr int kRows = 16;    // query rows of an item (one m16 matrix instructio
 constexpr int kKeys = 64;    // positions of a tile
 constexpr int kWarps = 4;    // each takes kKeys / kWarps positions of a tile
 constexpr int kStages = 3;   // tiles in shared memory
+constexpr int kBlocksPerSm = 2;  // of the partial kernel, as many as fit at once
 constexpr int kMaxRowsB = 1024;
 
 struct AttnDev {
@@ -36,6 +37,7 @@ struct AttnDev {
   int32_t *status;
   long long q_bs, q_ts, q_hs, o_bs, o_ts, o_hs, kv_ps, kv_hs, kv_rs;  // bytes
   int B, T, nq, nkv, G, page, n_pages, n_prefix_pages, table_width;
+  int page_shift;  // log2(page), or -1
   float scale2;  // |scale| * log2(e): scores in powers of two
   uint32_t flip; // sign bits of two elements of q: set for a negative scale
   int n_prefix_items, own_tiles, n_items;  // items: prefix [kv head][row tile], then own [b][kv head][row tile]
@@ -132,6 +134,28 @@ __device__ __forceinline__ float exp2_(float x) {
   return y;
 }
 
+// two 32-bit numbers in a register pair
+__device__ __forceinline__ unsigned long long pack2(float x, float y) {
+  unsigned long long r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(x), "f"(y));
+  return r;
+}
+__device__ __forceinline__ float2 unpack2(unsigned long long v) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
+  return r;
+}
+__device__ __forceinline__ unsigned long long fma2(unsigned long long a, unsigned long long b, unsigned long long c) {
+  unsigned long long r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ unsigned long long add2(unsigned long long a, unsigned long long b) {
+  unsigned long long r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+
 template <class T>
 struct Num;
 template <>
@@ -171,8 +195,8 @@ struct Num<__half> {
   }
 };
 
-// Shared memory of the partial kernel: the tiles (K then V of each stage),
-// reused at an item's end for the warps' partials; then the line's sums.
+// Shared memory of the partial kernel: each warp's stages (its rows of K, then
+// of V), reused at an item's end for the warps' partials; then the line's sums.
 template <int D>
 constexpr int tile_bytes() {
   return kKeys * D * 2;
@@ -190,14 +214,31 @@ __device__ __forceinline__ uint32_t at(int r, int c) {
   return (uint32_t)(r * (D * 2) + ((c ^ (r & 7)) << 4));
 }
 
+// Where a position's row is: byte offset into K or V of the row's head 0.
+__device__ __forceinline__ long long row_offset(const AttnDev &p, const int *list, int pos) {
+  const int pi = p.page_shift >= 0 ? pos >> p.page_shift : pos / p.page;
+  int pg = list[pi];
+  if ((unsigned)pg >= (unsigned)p.n_pages) {
+    report(p.status, MK_ERR_DEVICE_INPUT);
+    pg = 0;
+  }
+  return pg * p.kv_ps + (pos - pi * p.page) * p.kv_rs;
+}
+
+// The warps of a block work on their own: warp w copies, and attends over, the
+// positions 16 w .. 16 w + 15 of every tile, kStages tiles deep, without a
+// barrier until an item's end.  A lane looks up the page of one position, a
+// tile ahead of the copies that need it.
 template <class T, int D>
-__global__ void __launch_bounds__(kWarps * 32) part_kernel(const AttnDev p) {
+__global__ void __launch_bounds__(kWarps * 32, kBlocksPerSm) part_kernel(const AttnDev p) {
   extern __shared__ __align__(128) char sm[];
   __shared__ int red[kWarps];
   __shared__ float m_s[kWarps][kRows], l_s[kWarps][kRows];
   int *sum = reinterpret_cast<int *>(sm + smem_tiles<D>());
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const uint32_t sm0 = smem_addr(sm);
+  constexpr int kHalf = kRows * D * 2, kStage = 2 * kHalf;  // bytes of a warp's 16 rows of K; of K and V
+  char *const mine = sm + warp * kStages * kStage;
+  const uint32_t mine_a = smem_addr(mine);
   // Behind the tensor-core kernel this one starts as blocks of that one end;
   // it reads nothing of its, and only waits for it before it ends itself.
   if (!p.tc_rows) pdl_wait();
@@ -234,7 +275,7 @@ __global__ void __launch_bounds__(kWarps * 32) part_kernel(const AttnDev p) {
       b = x0;
       const int nt = sum[b + 1] - sum[b];
       const long long base = line.own0 + (long long)sum[b] * per;
-      const int k = (int)((t0 - base) / nt);
+      const int k = (int)(t0 - base) / nt;
       item = p.n_prefix_items + b * per + k;
       item_t0 = base + (long long)k * nt;
       item_t1 = item_t0 + nt;
@@ -246,6 +287,34 @@ __global__ void __launch_bounds__(kWarps * 32) part_kernel(const AttnDev p) {
     }
     const int first = (int)(t0 - item_t0), n_tiles = (int)(min(t_end, item_t1) - t0);
     t0 += n_tiles;
+
+    const int *table = p.table + (long long)b * p.table_width;  // (not used by prefix items)
+    const int key0 = lo + first * kKeys + warp * 16;  // this warp's first position
+    auto look_up = [&](int i) {  // where this lane's position of tile i is (lanes 16-31: as 0-15)
+      const int pos = key0 + i * kKeys + (lane & 15);
+      return i < n_tiles && pos < hi ? row_offset(p, pos < line.prefix ? p.prefix_pages : table, pos) : 0ll;
+    };
+    auto load = [&](int i, long long off) {  // tile i into stage i % kStages
+      const uint32_t dst = mine_a + (i % kStages) * kStage;
+      constexpr int kChunks = D / 8, kPass = 32 / kChunks;  // rows of one instruction
+      const int ch = lane % kChunks, r0 = lane / kChunks, left = hi - (key0 + i * kKeys);
+#pragma unroll
+      for (int x = 0; x < 16 / kPass; ++x) {
+        const int r = x * kPass + r0;
+        const long long o = __shfl_sync(0xffffffffu, off, r) + kv * p.kv_hs + ch * 16;
+        const bool live = r < left;
+        cp16(dst + at<D>(r, ch), p.k + o, live);
+        cp16(dst + kHalf + at<D>(r, ch), p.v + o, live);
+      }
+    };
+    long long off = look_up(0);
+#pragma unroll
+    for (int i = 0; i < kStages - 1; ++i) {
+      const long long next = look_up(i + 1);
+      if (i < n_tiles) load(i, off);
+      cp_commit();
+      off = next;
+    }
 
     // ---- this thread's rows: r and r + 8 of the tile (g = lane / 4)
     auto row_of = [&](int r, int &rb, int &rt, int &rh) {
@@ -277,54 +346,27 @@ __global__ void __launch_bounds__(kWarps * 32) part_kernel(const AttnDev p) {
     }
     min_sees = __reduce_min_sync(0xffffffffu, min_sees);
 
-    const int *table = p.table + (long long)b * p.table_width;  // (not used by prefix items)
-    auto load_tile = [&](int i) {  // tile first + i into stage i % kStages
-      const uint32_t dst = sm0 + (i % kStages) * 2 * tile_bytes<D>();
-      const int pos0 = lo + (first + i) * kKeys;
-      constexpr int kChunks = D / 8, kPerPass = kWarps * 32 / kChunks;  // rows of one pass of the block
-#pragma unroll
-      for (int x = 0; x < kKeys / kPerPass; ++x) {
-        const int r = x * kPerPass + tid / kChunks, ch = tid % kChunks, pos = pos0 + r;
-        const bool live = pos < hi;
-        long long off = 0;
-        if (live) {
-          const int pi = pos / p.page;
-          int pg = pos < line.prefix ? p.prefix_pages[pi] : table[pi];
-          if ((unsigned)pg >= (unsigned)p.n_pages) {
-            report(p.status, MK_ERR_DEVICE_INPUT);
-            pg = 0;
-          }
-          off = (long long)pg * p.kv_ps + kv * p.kv_hs + (pos - pi * p.page) * p.kv_rs + ch * 16;
-        }
-        cp16(dst + at<D>(r, ch), p.k + off, live);
-        cp16(dst + tile_bytes<D>() + at<D>(r, ch), p.v + off, live);
-      }
-    };
-
     float o[D / 8][4], m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
 #pragma unroll
     for (int i = 0; i < D / 8; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
 
-#pragma unroll
-    for (int i = 0; i < kStages - 1; ++i) {
-      if (i < n_tiles) load_tile(i);
-      cp_commit();
-    }
     for (int i = 0; i < n_tiles; ++i) {
+      const long long next = look_up(i + kStages);
       cp_wait<kStages - 2>();
-      __syncthreads();
-      if (i + kStages - 1 < n_tiles) load_tile(i + kStages - 1);
+      __syncwarp();
+      if (i + kStages - 1 < n_tiles) load(i + kStages - 1, off);
       cp_commit();
-      const uint32_t kt = sm0 + (i % kStages) * 2 * tile_bytes<D>(), vt = kt + tile_bytes<D>();
-      const int key0 = warp * (kKeys / kWarps);  // this warp's 16 positions of the tile
-      const int pos0 = lo + (first + i) * kKeys + key0;
+      off = next;
+      const int pos0 = key0 + i * kKeys;
       if (pos0 >= hi) continue;
+      const char *kt = mine + (i % kStages) * kStage, *vt = kt + kHalf;
+      const uint32_t ka = smem_addr(kt), va = ka + kHalf;
       // ---- scores: 16 rows x 16 positions
       float s[2][4] = {};
 #pragma unroll
       for (int k = 0; k < D / 16; ++k) {
         uint32_t kf[4];  // positions 0-7 and 8-15, elements 0-7 and 8-15 of this step
-        ldsm4(kf, kt + at<D>(key0 + (lane & 7) + (lane >> 4) * 8, k * 2 + ((lane >> 3) & 1)));
+        ldsm4(kf, ka + at<D>((lane & 7) + (lane >> 4) * 8, k * 2 + ((lane >> 3) & 1)));
         Num<T>::mma(s[0], qf[k], kf[0], kf[1]);
         Num<T>::mma(s[1], qf[k], kf[2], kf[3]);
       }
@@ -372,7 +414,7 @@ __global__ void __launch_bounds__(kWarps * 32) part_kernel(const AttnDev p) {
 #pragma unroll
         for (int x = 0; x < D / 16; ++x) {
           const int id = x * 32 + lane;
-          const uint4 w = *reinterpret_cast<const uint4 *>(sm + (vt - sm0) + at<D>(key0 + id / (D / 8), id % (D / 8)));
+          const uint4 w = *reinterpret_cast<const uint4 *>(vt + at<D>(id / (D / 8), id % (D / 8)));
           odd |= !(Num<T>::finite2(w.x) && Num<T>::finite2(w.y) && Num<T>::finite2(w.z) && Num<T>::finite2(w.w));
         }
         if (__any_sync(0xffffffffu, odd)) {
@@ -385,7 +427,7 @@ __global__ void __launch_bounds__(kWarps * 32) part_kernel(const AttnDev p) {
 #pragma unroll
               for (int d = 0; d < D / 8; ++d) {
                 const float2 v = Num<T>::unpack(
-                    *reinterpret_cast<const uint32_t *>(sm + (vt - sm0) + at<D>(key0 + j, d) + (lane & 3) * 4));
+                    *reinterpret_cast<const uint32_t *>(vt + at<D>(j, d) + (lane & 3) * 4));
                 o[d][2 * h] = fmaf(w, v.x, o[d][2 * h]);
                 o[d][2 * h + 1] = fmaf(w, v.y, o[d][2 * h + 1]);
               }
@@ -407,7 +449,7 @@ __global__ void __launch_bounds__(kWarps * 32) part_kernel(const AttnDev p) {
 #pragma unroll
       for (int d = 0; d < D / 16; ++d) {
         uint32_t vf[4];  // positions 0-7 and 8-15 of columns 0-7, then of columns 8-15
-        ldsm4t(vf, vt + at<D>(key0 + (lane & 15), d * 2 + (lane >> 4)));
+        ldsm4t(vf, va + at<D>(lane & 15, d * 2 + (lane >> 4)));
         Num<T>::mma(o[2 * d], ph, vf[0], vf[1]);
         Num<T>::mma(o[2 * d], pl, vf[0], vf[1]);
         Num<T>::mma(o[2 * d + 1], ph, vf[2], vf[3]);
@@ -482,7 +524,6 @@ __global__ void __launch_bounds__(kWarps * 32) part_kernel(const AttnDev p) {
 constexpr int kTcRows = 128;  // rows of a half
 constexpr int kTcKeys = 128;  // positions of a tile
 constexpr int kTcThreads = 13 * 32;  // warps 0-3 and 4-7: softmax; 8-11: copies; 12: matrix instructions
-constexpr int kTcLag = 2;     // copies of a tile stay in flight behind this many later ones
 constexpr float kTcGrow = 8.f;
 template <int D>
 constexpr int tc_tile() {
@@ -601,6 +642,11 @@ __device__ bool bar_wait(TcShared *sh, uint64_t *b, uint32_t parity, int32_t *st
   return true;
 }
 
+// Arrive on b when this thread's copies so far have landed.
+__device__ __forceinline__ void cp_arrive(uint64_t *b) {
+  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_addr(b)) : "memory");
+}
+
 // The blocks' line of tiles, as for the other items.
 struct TcLine {
   int prefix, tiles, n_items;
@@ -627,7 +673,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) tc_kernel(const AttnDev p) {
   const uint32_t ring = base + 2 * tc_tile<D>();
   if (tid == 0) {
     for (int i = 0; i < kRing; ++i) {
-      bar_init(&sh.full[i], 4);
+      bar_init(&sh.full[i], 128);
       bar_init(&sh.empty[i], 1);
     }
     for (int w = 0; w < 2; ++w) {
@@ -658,66 +704,50 @@ __global__ void __launch_bounds__(kTcThreads, 1) tc_kernel(const AttnDev p) {
   auto o_of = [&](int w) { return tm + 256 + w * D; };
 
   if (warp >= 8 && warp < 12) {
-    // ---------------- copies
-    int g = 0, told = 0;  // ring entries begun; of which announced
+    // ---------------- copies: warp w of the four takes rows 32 w .. 32 w + 31
+    // of every tile; a lane looks up the page of one, an entry ahead
+    int g = 0;  // ring entries begun
     bool ok = true;
-    const int t = tid - 256;
-    auto tell = [&](int upto) {  // this warp's part of the entries before `upto` has landed
-      fence_smem_async();
-      __syncwarp();
-      if (lane == 0)
-        for (int i = told; i < upto; ++i) bar_arrive(&sh.full[i % kRing]);
-      told = max(told, upto);
-    };
+    const int row = (warp - 8) * 32;
     for (long long t0 = t_begin; ok && t0 < t_end;) {
       const int item = (int)(t0 / line.tiles), first = (int)(t0 % line.tiles);
       const int n = (int)min(t_end - t0, (long long)(line.tiles - first)), kv = item / p.tc_groups;
       t0 += n;
-      auto put = [&](const char *src, int j) {
-        const int slot = g % kRing;
-        if (!ok) return;
-        const uint32_t phase = ((g / kRing) & 1) ^ 1;
-        if (g >= kRing && !__all_sync(0xffffffffu, bar_try(&sh.empty[slot], phase))) {
-          cp_wait<0>();  // nothing is held back while this warp waits
-          tell(g);
-          ok = __all_sync(0xffffffffu, bar_wait(&sh, &sh.empty[slot], phase, p.status));
-          if (!ok) return;
-        }
-        const uint32_t dst = ring + slot * tc_tile<D>();
-        constexpr int kChunks = D / 8, kPass = 128 / kChunks;
-        const int ch = t % kChunks, pos0 = (first + j) * kTcKeys + t / kChunks;
-        const char *from = src + kv * p.kv_hs + ch * 16;
-#pragma unroll 4
-        for (int x = 0; x < kTcKeys / kPass; ++x) {
-          const int pos = pos0 + x * kPass;
-          const bool live = pos < line.prefix;
-          long long off = 0;
-          if (live) {
-            const int pi = pos / p.page;
-            int pg = p.prefix_pages[pi];
-            if ((unsigned)pg >= (unsigned)p.n_pages) {
-              report(p.status, MK_ERR_DEVICE_INPUT);
-              pg = 0;
-            }
-            off = (long long)pg * p.kv_ps + (pos - pi * p.page) * p.kv_rs;
-          }
-          cp16(dst + tc_at(x * kPass + t / kChunks, ch), from + off, live);
-        }
-        cp_commit();
-        ++g;
-        if (g - told > kTcLag) {
-          cp_wait<kTcLag>();
-          tell(g - kTcLag);
-        }
+      auto look_up = [&](int j) {
+        const int pos = (first + j) * kTcKeys + row + lane;
+        return j < n && pos < line.prefix ? row_offset(p, p.prefix_pages, pos) : 0ll;
       };
-      for (int j = 0; j < min(dist, n); ++j) put(p.k, j);
-      for (int j = 0; j < n; ++j) {
-        put(p.v, j);
-        if (j + dist < n) put(p.k, j + dist);
+      auto put = [&](const char *src, int j, long long off) {
+        const int slot = g % kRing;
+        if (g >= kRing) ok = __all_sync(0xffffffffu, bar_wait(&sh, &sh.empty[slot], ((g / kRing) & 1) ^ 1, p.status));
+        if (!ok) return;
+        const uint32_t dst = ring + slot * tc_tile<D>();
+        constexpr int kChunks = D / 8, kPass = 32 / kChunks;
+        const int ch = lane % kChunks, r0 = lane / kChunks, left = line.prefix - (first + j) * kTcKeys - row;
+        const char *from = src + kv * p.kv_hs + ch * 16;
+#pragma unroll
+        for (int x = 0; x < 32 / kPass; ++x) {
+          const int r = x * kPass + r0;
+          const long long o = __shfl_sync(0xffffffffu, off, r);
+          cp16(dst + tc_at(row + r, ch), from + o, r < left);
+        }
+        cp_arrive(&sh.full[slot]);
+        ++g;
+      };
+      // K tiles run `dist` ahead of their V
+      long long now = look_up(0), next = look_up(1);
+      put(p.k, 0, now);
+      if (dist == 2 && n > 1) put(p.k, 1, next);
+      for (int j = 0; ok && j < n; ++j) {
+        const long long later = look_up(j + 2);
+        put(p.v, j, now);
+        if (j + dist < n) put(p.k, j + dist, dist == 1 ? next : later);
+        now = next;
+        next = later;
       }
     }
+    cp_commit();
     cp_wait<0>();
-    tell(g);
   } else if (warp == 12) {
     // ---------------- matrix instructions
     if (lane == 0) {
@@ -732,6 +762,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) tc_kernel(const AttnDev p) {
       auto take = [&]() {  // the next ring entry's tile
         const int slot = g % kRing;
         ok = ok && bar_wait(&sh, &sh.full[slot], (g / kRing) & 1, p.status);
+        fence_smem_async();  // the copies' writes, before the tensor cores' reads
         ++g;
         return slot;
       };
@@ -876,18 +907,24 @@ __global__ void __launch_bounds__(kTcThreads, 1) tc_kernel(const AttnDev p) {
         if (any_live) {
           const int valid = min(kTcKeys, line.prefix - (first + j) * kTcKeys);
           const uint32_t s = s_of(w) + lanes;
-          uint32_t x[32];
+          // S is read twice, 32 columns at a time, each read begun while the
+          // columns before it are worked on
+          uint32_t x[2][32];
           float top = -INFINITY;
+          tm_ld32(s, x[0]);
 #pragma unroll
           for (int q = 0; q < 4; ++q) {
-            tm_ld32(s + q * 32, x);
             tm_wait_ld();
+            tm_ld32(s + (q + 1) % 4 * 32, x[(q + 1) & 1]);
+            const uint32_t(&y)[32] = x[q & 1];
             if (valid >= kTcKeys) {
+              float t[4] = {top, top, top, top};
 #pragma unroll
-              for (int i = 0; i < 32; ++i) top = fmaxf(top, __uint_as_float(x[i]));
+              for (int i = 0; i < 32; ++i) t[i & 3] = fmaxf(t[i & 3], __uint_as_float(y[i]));
+              top = fmaxf(fmaxf(t[0], t[1]), fmaxf(t[2], t[3]));
             } else {
 #pragma unroll
-              for (int i = 0; i < 32; ++i) top = q * 32 + i < valid ? fmaxf(top, __uint_as_float(x[i])) : top;
+              for (int i = 0; i < 32; ++i) top = q * 32 + i < valid ? fmaxf(top, __uint_as_float(y[i])) : top;
             }
           }
           top = top == -INFINITY ? top : top * p.scale2;
@@ -900,38 +937,46 @@ __global__ void __launch_bounds__(kTcThreads, 1) tc_kernel(const AttnDev p) {
               const float f = grow ? exp2_(m - top) : 1.f;
               if (grow) m = top;
               l *= f;
+              tm_wait_ld();  // (x[0]: the first columns, read again)
               for (int q = 0; q < D / 32; ++q) {
-                tm_ld32(o_of(w) + lanes + q * 32, x);
+                tm_ld32(o_of(w) + lanes + q * 32, x[1]);
                 tm_wait_ld();
 #pragma unroll
-                for (int i = 0; i < 32; ++i) x[i] = __float_as_uint(__uint_as_float(x[i]) * f);
-                tm_st32(o_of(w) + lanes + q * 32, x);
+                for (int i = 0; i < 32; ++i) x[1][i] = __float_as_uint(__uint_as_float(x[1][i]) * f);
+                tm_st32(o_of(w) + lanes + q * 32, x[1]);
               }
             }
           }
           const float b = m == -INFINITY ? 0.f : m;
-          float sum0 = 0.f, sum1 = 0.f;
+          const unsigned long long scale = pack2(p.scale2, p.scale2), minus = pack2(-b, -b);
+          unsigned long long sum = 0ull;
 #pragma unroll
           for (int q = 0; q < 4; ++q) {
-            tm_ld32(s + q * 32, x);
             tm_wait_ld();
+            if (q < 3) tm_ld32(s + (q + 1) * 32, x[(q + 1) & 1]);
+            const uint32_t(&y)[32] = x[q & 1];
             uint32_t h[16];
+            if (valid >= kTcKeys) {
 #pragma unroll
-            for (int i = 0; i < 32; i += 2) {
-              float a0 = __uint_as_float(x[i]), a1 = __uint_as_float(x[i + 1]);
-              if (valid < kTcKeys) {
-                a0 = q * 32 + i < valid ? a0 : -INFINITY;
-                a1 = q * 32 + i + 1 < valid ? a1 : -INFINITY;
+              for (int i = 0; i < 32; i += 2) {
+                const float2 t = unpack2(fma2(pack2(__uint_as_float(y[i]), __uint_as_float(y[i + 1])), scale, minus));
+                const float e0 = exp2_(t.x), e1 = exp2_(t.y);
+                sum = add2(sum, pack2(e0, e1));
+                h[i / 2] = Num<T>::pack(e0, e1);
               }
-              const float e0 = a0 == -INFINITY ? 0.f : exp2_(fmaf(a0, p.scale2, -b));
-              const float e1 = a1 == -INFINITY ? 0.f : exp2_(fmaf(a1, p.scale2, -b));
-              sum0 += e0;
-              sum1 += e1;
-              h[i / 2] = Num<T>::pack(e0, e1);
+            } else {
+#pragma unroll
+              for (int i = 0; i < 32; i += 2) {
+                const float e0 = q * 32 + i < valid ? exp2_(fmaf(__uint_as_float(y[i]), p.scale2, -b)) : 0.f;
+                const float e1 = q * 32 + i + 1 < valid ? exp2_(fmaf(__uint_as_float(y[i + 1]), p.scale2, -b)) : 0.f;
+                sum = add2(sum, pack2(e0, e1));
+                h[i / 2] = Num<T>::pack(e0, e1);
+              }
             }
             tm_st16(s + q * 16, h);
           }
-          l += sum0 + sum1;
+          const float2 both = unpack2(sum);
+          l += both.x + both.y;
           tm_wait_st();
         }
         tc_before();
@@ -1026,35 +1071,47 @@ __global__ void __launch_bounds__(128) join_kernel(const AttnDev p, int N, int t
       return i < n_pre ? (s_pre + i) * kRows + pr % kRows : (s_own + i - n_pre) * kRows + r_own;
     };
     auto ml_of = [&](int i) { return i < n_tc ? p.tc_ml[tc_slot(i) * kTcRows + r_tc % kTcRows] : p.part_ml[part_row(i)]; };
+    constexpr int kWays = 128 / D;
+    const int d4 = lane % (D / 4), way = lane / (D / 4);
     float M = -INFINITY, L = 0.f;
-    for (int i = lane; i < n; i += 32) {
-      const float2 ml = ml_of(i);
-      if (ml.y != 0.f) M = fmaxf(M, ml.x);
-    }
+    float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int i0 = 0; i0 < n; i0 += 32) {  // 32 partials at a time, a lane looking at each
+      const int k = min(32, n - i0);
+      const float2 ml = lane < k ? ml_of(i0 + lane) : make_float2(-INFINITY, 0.f);
+      float top = ml.y != 0.f ? ml.x : -INFINITY;
 #pragma unroll
-    for (int o = 16; o; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
-    const float base = M == -INFINITY ? 0.f : M;
-    for (int i = lane; i < n; i += 32) {
-      const float2 ml = ml_of(i);
-      if (ml.y != 0.f) L += ml.y * exp2_(ml.x - base);
+      for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+      const float old = M;
+      M = fmaxf(M, top);
+      const float base = M == -INFINITY ? 0.f : M, scale = exp2_(old - base);
+      // (a partial without a sum has nothing, and its o was not written)
+      const bool there = ml.y != 0.f;
+      const float f = there ? exp2_(ml.x - base) : 0.f;
+      const unsigned some = __ballot_sync(0xffffffffu, there);
+      L = L * scale + f * ml.y;
+      a.x *= scale;
+      a.y *= scale;
+      a.z *= scale;
+      a.w *= scale;
+      // (loads that wait for nothing: from the last partial where there is no other)
+      auto add = [&](int i, int end, const float4 &y) {
+        const float w = __shfl_sync(0xffffffffu, f, (i + way) & 31);
+        const bool use = i + way < end && (some >> ((i + way) & 31) & 1);
+        a.x += use ? w * y.x : 0.f;
+        a.y += use ? w * y.y : 0.f;
+        a.z += use ? w * y.z : 0.f;
+        a.w += use ? w * y.w : 0.f;
+      };
+      const int k_tc = max(0, min(k, n_tc - i0));
+#pragma unroll 8
+      for (int i = 0; i < k_tc; i += kWays)
+        add(i, k_tc, p.tc_o[(tc_slot(min(i0 + i + way, n_tc - 1)) * (D / 4) + d4) * kTcRows + r_tc % kTcRows]);
+#pragma unroll 4
+      for (int i = k_tc; i < k; i += kWays)
+        add(i, k, *reinterpret_cast<const float4 *>(p.part_o + part_row(min(i0 + i + way, n - 1)) * D + d4 * 4));
     }
 #pragma unroll
     for (int o = 16; o; o >>= 1) L += __shfl_xor_sync(0xffffffffu, L, o);
-    constexpr int kWays = 128 / D;
-    const int d4 = lane % (D / 4);
-    float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-    for (int i = lane / (D / 4); i < n; i += kWays) {
-      const float2 ml = ml_of(i);
-      if (ml.y == 0.f) continue;  // nothing there (its o was not written)
-      const float f = exp2_(ml.x - base);
-      const float4 y = i < n_tc ? p.tc_o[(tc_slot(i) * (D / 4) + d4) * kTcRows + r_tc % kTcRows]
-                                : *reinterpret_cast<const float4 *>(p.part_o + part_row(i) * D + d4 * 4);
-      a.x += f * y.x;
-      a.y += f * y.y;
-      a.z += f * y.z;
-      a.w += f * y.w;
-    }
     if (kWays == 2) {
       a.x += __shfl_xor_sync(0xffffffffu, a.x, 16);
       a.y += __shfl_xor_sync(0xffffffffu, a.y, 16);
@@ -1084,7 +1141,6 @@ int check(const mk_attn_shared_args *a) {
   return MK_OK;
 }
 
-constexpr int kBlocksPerSm = 2;  // of the partial kernel, as many as fit at once
 constexpr int kTcMinRows = 17;   // rows of a K/V head from which the prefix goes to the tensor cores' kernel
 
 void fill(const mk_attn_shared_args *a, AttnDev *d) {
@@ -1187,6 +1243,7 @@ extern "C" int mk_attn_shared(const mk_attn_shared_args *a, void *workspace, voi
   d.kv_rs = 2 * a->row_stride;
   d.page = a->page;
   d.n_pages = a->n_pages;
+  d.page_shift = (a->page & (a->page - 1)) == 0 ? __builtin_ctz((unsigned)a->page) : -1;
   d.n_prefix_pages = a->n_prefix_pages;
   d.table_width = a->table_width;
   d.scale2 = (float)(std::fabs((double)a->scale) * 1.4426950408889634);

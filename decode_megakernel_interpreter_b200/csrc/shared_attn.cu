@@ -506,15 +506,15 @@ __global__ void __launch_bounds__(kWarps * 32, kBlocksPerSm) part_kernel(const A
 
 // ---------------------------------------------------------------- the prefix on the tensor cores
 //
-// S = Q K^T and O += P V as 128 x 128 matrix instructions (tcgen05, operands in
-// shared memory, accumulators in tensor memory).  A block has two halves of
-// four softmax warps, a row per thread, each half with its own S, O, m and l:
+// S = Q K^T and O += P V as matrix instructions of 128 rows (tcgen05, operands
+// in shared memory, accumulators in tensor memory).  A block has two halves of
+// four softmax warps, a row per thread, each half with its own O, m and l:
 //   tc_rows = 256: the halves take 128 rows each and read the same K/V tiles;
 //   tc_rows = 128: both take the same rows, and every other K/V tile.
-// One half's softmax thus runs while the tensor cores work for the other.
-// Four warps copy the K/V tiles (16 bytes a time, rows from the page list) into
-// a ring in the order they are needed, and one thread issues the matrix
-// instructions.
+// Each half has two S of 64 positions: the tensor cores fill one while the
+// softmax works on the other.  Four warps copy the K/V tiles (16 bytes a time,
+// rows from the page list) into a ring in the order they are needed, and one
+// thread issues the matrix instructions.
 // P takes S's place in tensor memory, rounded to the operands' type: half a
 // step (2^-8 or 2^-11) of each weight, as the output's own rounding.
 // A row's maximum only moves when it grows by more than 2^8: until then the
@@ -522,7 +522,7 @@ __global__ void __launch_bounds__(kWarps * 32, kBlocksPerSm) part_kernel(const A
 // need not be rescaled.
 
 constexpr int kTcRows = 128;  // rows of a half
-constexpr int kTcKeys = 128;  // positions of a tile
+constexpr int kTcKeys = 64;   // positions of a tile
 constexpr int kTcThreads = 13 * 32;  // warps 0-3 and 4-7: softmax; 8-11: copies; 12: matrix instructions
 constexpr float kTcGrow = 8.f;
 template <int D>
@@ -531,25 +531,33 @@ constexpr int tc_tile() {
 }
 template <int D>
 constexpr int tc_ring() {
-  return D == 128 ? 5 : 10;  // tiles of K or V in flight or in use: 160 KB
+  return D == 128 ? 10 : 16;  // tiles of K or V in flight or in use
 }
 template <int D>
 constexpr int tc_smem() {
-  return (2 + tc_ring<D>()) * tc_tile<D>() + 1024;
+  return 2 * kTcRows * D * 2 + tc_ring<D>() * tc_tile<D>() + 1024;
 }
 
-// Byte of element chunk c (8 elements) of row r in a tile of 128 rows: 64
+// Byte of element chunk c (8 elements) of row r in a tile of `rows` rows: 64
 // elements (128 bytes) of every row, then the next 64; the eight chunks of 128
 // bytes exchanged by the row number (the 128-byte swizzle of the operand
 // descriptors).
-__device__ __forceinline__ uint32_t tc_at(int r, int c) {
-  return (uint32_t)((c >> 3) * (kTcKeys * 128) + r * 128 + (((c & 7) ^ (r & 7)) << 4));
+__device__ __forceinline__ uint32_t tc_at(int rows, int r, int c) {
+  return (uint32_t)((c >> 3) * (rows * 128) + r * 128 + (((c & 7) ^ (r & 7)) << 4));
 }
-// Operand descriptor: 128-byte swizzle, 8-row groups 1024 bytes apart; lbo: from
-// 64 elements of the leading dimension to the next 64 (read for V only).
-__device__ __forceinline__ uint64_t tc_desc(uint32_t addr, uint32_t lbo) {
-  return (uint64_t)((addr >> 4) & 0x3FFFu) | ((uint64_t)((lbo >> 4) & 0x3FFFu) << 16) | ((uint64_t)(1024 >> 4) << 32) |
-         (1ull << 46) | (2ull << 61);
+// Operand descriptor: 128-byte swizzle, 8-row groups 1024 bytes apart.  Its low
+// word is the address and lbo (from 64 elements of the leading dimension to the
+// next 64; read for V only), in units of 16 bytes; the high word is the same
+// for all, so that a step through a tile is one addition.
+__device__ __forceinline__ uint32_t tc_low(uint32_t addr, uint32_t lbo) { return (addr >> 4) | (lbo >> 4) << 16; }
+__device__ __forceinline__ uint64_t tc_desc(uint32_t low) {
+  constexpr uint32_t high = (1024u >> 4) | (1u << 14) | (2u << 29);
+  return (uint64_t)high << 32 | low;
+}
+__device__ __forceinline__ bool elect_one() {
+  uint32_t r;
+  asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}\n" : "=r"(r));
+  return r != 0;
 }
 __device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool add) {
   asm volatile(
@@ -579,6 +587,14 @@ __device__ __forceinline__ void tm_ld32(uint32_t a, uint32_t (&r)[32]) {
         "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
         "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
         "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+      : "r"(a)
+      : "memory");
+}
+__device__ __forceinline__ void tm_ld16(uint32_t a, uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
       : "r"(a)
       : "memory");
 }
@@ -620,15 +636,14 @@ __device__ __forceinline__ bool bar_try(uint64_t *b, uint32_t parity) {
 
 struct TcShared {
   uint64_t full[16], empty[16];  // ring entries
-  uint64_t q_full[2], s_full[2], p_full[2], o_full[2], drain;
+  uint64_t q_full[2], s_full[2][2], p_full[2][2], o_full[2], drain;  // [half][which S]; o_full: a P V is complete
   uint32_t tmem;
   volatile int dead;  // a wait gave up
 };
 
 // Wait for a phase; false when it does not come within a second (or another
 // wait has given up): every role then runs to the kernel's end.
-__device__ bool bar_wait(TcShared *sh, uint64_t *b, uint32_t parity, int32_t *status) {
-  if (bar_try(b, parity)) return true;
+__device__ __noinline__ bool bar_wait_long(TcShared *sh, uint64_t *b, uint32_t parity, int32_t *status) {
   uint64_t t0, t;
   asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t0));
   while (!bar_try(b, parity)) {
@@ -642,6 +657,13 @@ __device__ bool bar_wait(TcShared *sh, uint64_t *b, uint32_t parity, int32_t *st
   return true;
 }
 
+__device__ __forceinline__ bool bar_wait(TcShared *sh, uint64_t *b, uint32_t parity, int32_t *status) {
+  return bar_try(b, parity) || bar_wait_long(sh, b, parity, status);
+}
+// the same by a whole warp
+__device__ __forceinline__ bool bar_wait_all(TcShared *sh, uint64_t *b, uint32_t parity, int32_t *status) {
+  return __all_sync(0xffffffffu, bar_wait(sh, b, parity, status));
+}
 // Arrive on b when this thread's copies so far have landed.
 __device__ __forceinline__ void cp_arrive(uint64_t *b) {
   asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_addr(b)) : "memory");
@@ -670,7 +692,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) tc_kernel(const AttnDev p) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const uint32_t base = (smem_addr(sm_raw) + 1023) & ~1023u;
   char *sm = sm_raw + (base - smem_addr(sm_raw));
-  const uint32_t ring = base + 2 * tc_tile<D>();
+  const uint32_t ring = base + 2 * kTcRows * D * 2;
   if (tid == 0) {
     for (int i = 0; i < kRing; ++i) {
       bar_init(&sh.full[i], 128);
@@ -678,8 +700,10 @@ __global__ void __launch_bounds__(kTcThreads, 1) tc_kernel(const AttnDev p) {
     }
     for (int w = 0; w < 2; ++w) {
       bar_init(&sh.q_full[w], 4);
-      bar_init(&sh.s_full[w], 1);
-      bar_init(&sh.p_full[w], 4);
+      for (int i = 0; i < 2; ++i) {
+        bar_init(&sh.s_full[w][i], 1);
+        bar_init(&sh.p_full[w][i], 4);
+      }
       bar_init(&sh.o_full[w], 1);
     }
     bar_init(&sh.drain, 1);
@@ -697,174 +721,160 @@ __global__ void __launch_bounds__(kTcThreads, 1) tc_kernel(const AttnDev p) {
   const TcLine line = tc_line(p, prefix_of(p), gridDim.x);
   const long long c = blockIdx.x;
   const bool pair = p.tc_rows == 2 * kTcRows;  // the halves have rows of their own
-  const int dist = pair ? 1 : 2;               // K tiles that are multiplied ahead of their V
+  const int dist = pair ? 2 : 4;               // K tiles that are multiplied ahead of their V
   const int R = p.B * p.T * p.G;
   const long long t_begin = c < line.N ? c * line.total / line.N : 0, t_end = c < line.N ? (c + 1) * line.total / line.N : 0;
-  auto s_of = [&](int w) { return tm + w * 128; };
+  auto s_of = [&](int w, int i) { return tm + w * 128 + i * 64; };
   auto o_of = [&](int w) { return tm + 256 + w * D; };
 
   if (warp >= 8 && warp < 12) {
-    // ---------------- copies: warp w of the four takes rows 32 w .. 32 w + 31
+    // ---------------- copies: warp w of the four takes rows 16 w .. 16 w + 15
     // of every tile; a lane looks up the page of one, an entry ahead
     int g = 0;  // ring entries begun
     bool ok = true;
-    const int row = (warp - 8) * 32;
+    const int row = (warp - 8) * 16;
     for (long long t0 = t_begin; ok && t0 < t_end;) {
       const int item = (int)(t0 / line.tiles), first = (int)(t0 % line.tiles);
       const int n = (int)min(t_end - t0, (long long)(line.tiles - first)), kv = item / p.tc_groups;
       t0 += n;
-      auto look_up = [&](int j) {
-        const int pos = (first + j) * kTcKeys + row + lane;
-        return j < n && pos < line.prefix ? row_offset(p, p.prefix_pages, pos) : 0ll;
+      // the order of use: K 0 .. dist - 1, then V j, K j + dist
+      const int ahead = min(dist, n);
+      auto tile_of = [&](int e) {  // entry e's tile; V: + 2^30
+        if (e < ahead) return e;
+        e -= ahead;
+        const int both = 2 * (n - ahead);
+        return e < both ? (e & 1 ? e / 2 + ahead : e / 2 + (1 << 30)) : e - (n - ahead) + (1 << 30);
       };
-      auto put = [&](const char *src, int j, long long off) {
-        const int slot = g % kRing;
-        if (g >= kRing) ok = __all_sync(0xffffffffu, bar_wait(&sh, &sh.empty[slot], ((g / kRing) & 1) ^ 1, p.status));
-        if (!ok) return;
+      auto look_up = [&](int e) {
+        const int pos = (first + (tile_of(e) & ~(1 << 30))) * kTcKeys + row + (lane & 15);
+        return e < 2 * n && pos < line.prefix ? row_offset(p, p.prefix_pages, pos) : 0ll;
+      };
+      long long next = look_up(0);
+      for (int e = 0; e < 2 * n; ++e) {
+        const long long off = next;
+        next = look_up(e + 1);
+        const int slot = g % kRing, j = tile_of(e);
+        if (g >= kRing) ok = bar_wait_all(&sh, &sh.empty[slot], ((g / kRing) & 1) ^ 1, p.status);
+        if (!ok) break;
         const uint32_t dst = ring + slot * tc_tile<D>();
         constexpr int kChunks = D / 8, kPass = 32 / kChunks;
-        const int ch = lane % kChunks, r0 = lane / kChunks, left = line.prefix - (first + j) * kTcKeys - row;
-        const char *from = src + kv * p.kv_hs + ch * 16;
+        const int ch = lane % kChunks, r0 = lane / kChunks, left = line.prefix - (first + (j & ~(1 << 30))) * kTcKeys - row;
+        const char *from = (j >> 30 ? p.v : p.k) + kv * p.kv_hs + ch * 16;
 #pragma unroll
-        for (int x = 0; x < 32 / kPass; ++x) {
+        for (int x = 0; x < 16 / kPass; ++x) {
           const int r = x * kPass + r0;
           const long long o = __shfl_sync(0xffffffffu, off, r);
-          cp16(dst + tc_at(row + r, ch), from + o, r < left);
+          cp16(dst + tc_at(kTcKeys, row + r, ch), from + o, r < left);
         }
         cp_arrive(&sh.full[slot]);
         ++g;
-      };
-      // K tiles run `dist` ahead of their V
-      long long now = look_up(0), next = look_up(1);
-      put(p.k, 0, now);
-      if (dist == 2 && n > 1) put(p.k, 1, next);
-      for (int j = 0; ok && j < n; ++j) {
-        const long long later = look_up(j + 2);
-        put(p.v, j, now);
-        if (j + dist < n) put(p.k, j + dist, dist == 1 ? next : later);
-        now = next;
-        next = later;
       }
     }
     cp_commit();
     cp_wait<0>();
   } else if (warp == 12) {
-    // ---------------- matrix instructions
-    if (lane == 0) {
-      constexpr uint32_t kType = sizeof(T) == 2 && std::is_same<T, __nv_bfloat16>::value ? 1u : 0u;
-      // 32-bit accumulators, both operands of this type, 128 rows; N = 128 positions, or N = D with V's
-      // leading dimension the other way round
-      constexpr uint32_t kS = (1u << 4) | (kType << 7) | (kType << 10) | ((128u / 8) << 17) | ((128u / 16) << 24);
-      constexpr uint32_t kO = (1u << 4) | (kType << 7) | (kType << 10) | (1u << 16) | ((uint32_t)(D / 8) << 17) | ((128u / 16) << 24);
-      int g = 0;                       // ring entries used
-      uint32_t q_phase[2] = {0, 0}, p_phase[2] = {0, 0};
-      bool ok = true;
-      auto take = [&]() {  // the next ring entry's tile
-        const int slot = g % kRing;
-        ok = ok && bar_wait(&sh, &sh.full[slot], (g / kRing) & 1, p.status);
-        fence_smem_async();  // the copies' writes, before the tensor cores' reads
-        ++g;
-        return slot;
-      };
-      for (long long t0 = t_begin; ok && t0 < t_end;) {
-        const int item = (int)(t0 / line.tiles), first = (int)(t0 % line.tiles);
-        const int n = (int)min(t_end - t0, (long long)(line.tiles - first));
-        t0 += n;
-        const int row0 = item % p.tc_groups * p.tc_rows;
-        const bool two = pair && row0 + kTcRows < R;  // the second half has rows
-        for (int w = 0; w < 2; ++w)  // the halves that have tiles here
-          if (w == 0 || (pair ? two : n > 1)) {
-            ok = ok && bar_wait(&sh, &sh.q_full[w], q_phase[w], p.status);
-            q_phase[w] ^= 1;
-          }
-        if (!ok) break;
-        auto scores = [&](int w, int slot) {
-          const uint32_t q = base + w * tc_tile<D>(), k = ring + slot * tc_tile<D>();
-#pragma unroll
-          for (int i = 0; i < D / 16; ++i) {
-            const uint32_t o = (i / 4) * (kTcKeys * 128) + (i % 4) * 32;
-            mma_ss(s_of(w), tc_desc(q + o, 16), tc_desc(k + o, 16), kS, i > 0);
-          }
-          mma_commit(&sh.s_full[w]);
-        };
-        auto values = [&](int w, int slot, bool add) {
-          const uint32_t v = ring + slot * tc_tile<D>();
-#pragma unroll
-          for (int i = 0; i < kTcKeys / 16; ++i)
-            mma_ts(o_of(w), s_of(w) + i * 8, tc_desc(v + i * 2048, kTcKeys * 128), kO, add || i > 0);
-        };
-        auto weights = [&](int w) {  // half w has put P in S's place
-          ok = ok && bar_wait(&sh, &sh.p_full[w], p_phase[w], p.status);
-          p_phase[w] ^= 1;
-          tc_after();
-        };
-        if (pair) {
-          int k = take();
-          if (!ok) break;
-          scores(0, k);
-          if (two) scores(1, k);
-          mma_commit(&sh.empty[k]);
-          for (int j = 0; ok && j < n; ++j) {
-            const int v = take();
-            weights(0);
-            if (!ok) break;
-            values(0, v, j > 0);
-            if (j + 1 < n) {
-              k = take();
-              if (!ok) break;
-              scores(0, k);
-            } else {
-              mma_commit(&sh.o_full[0]);
-            }
-            if (two) {
-              weights(1);
-              if (!ok) break;
-              values(1, v, j > 0);
-            }
-            mma_commit(&sh.empty[v]);
-            if (j + 1 < n) {
-              if (two) scores(1, k);
-              mma_commit(&sh.empty[k]);
-            } else if (two) {
-              mma_commit(&sh.o_full[1]);
-            }
-          }
-        } else {
-          for (int j = 0; j < min(2, n); ++j) {
-            const int k = take();
-            if (!ok) break;
-            scores(j, k);
-            mma_commit(&sh.empty[k]);
-          }
-          for (int j = 0; ok && j < n; ++j) {
-            const int v = take();
-            weights(j & 1);
-            if (!ok) break;
-            values(j & 1, v, j > 1);
-            mma_commit(&sh.empty[v]);
-            if (j + 2 < n) {
-              const int k = take();
-              if (!ok) break;
-              scores(j & 1, k);
-              mma_commit(&sh.empty[k]);
-            } else {
-              mma_commit(&sh.o_full[j & 1]);
-            }
-          }
-        }
+    // ---------------- matrix instructions: the warp walks as one, an elected
+    // lane issues
+    constexpr uint32_t kType = std::is_same<T, __nv_bfloat16>::value ? 1u : 0u;
+    // 32-bit accumulators, both operands of this type, 128 rows; N = 64 positions, or N = D with V's
+    // leading dimension the other way round
+    constexpr uint32_t kS = (1u << 4) | (kType << 7) | (kType << 10) | ((kTcKeys / 8u) << 17) | ((128u / 16) << 24);
+    constexpr uint32_t kO = (1u << 4) | (kType << 7) | (kType << 10) | (1u << 16) | ((uint32_t)(D / 8) << 17) | ((128u / 16) << 24);
+    const uint32_t q_low = tc_low(base, 16), k_low = tc_low(ring, 16), v_low = tc_low(ring, kTcKeys * 128);
+    int slot = 0;                       // of the ring
+    uint32_t full_phase = 0, q_phase = 0, p_phase = 0;  // one bit; bit w; bit 2 w + i
+    bool ok = true;
+    auto take = [&]() {  // the next ring entry's tile
+      const int x = slot;
+      ok = ok && bar_wait_all(&sh, &sh.full[x], full_phase, p.status);
+      fence_smem_async();  // the copies' writes, before the tensor cores' reads
+      if (++slot == kRing) {
+        slot = 0;
+        full_phase ^= 1;
       }
-      if (!ok) {  // given up: the instructions in flight end before tensor memory goes
-        mma_commit(&sh.drain);
-        for (int i = 0; i < 100000 && !bar_try(&sh.drain, 0); ++i) {
+      return x;
+    };
+    auto scores = [&](int w, int i, int x) {
+      const uint32_t q = q_low + w * (kTcRows * D * 2 >> 4), k = k_low + x * (tc_tile<D>() >> 4);
+      if (elect_one()) {
+#pragma unroll
+        for (int e = 0; e < D / 16; ++e)
+          mma_ss(s_of(w, i), tc_desc(q + (e / 4 * (kTcRows * 128) + e % 4 * 32 >> 4)),
+                 tc_desc(k + (e / 4 * (kTcKeys * 128) + e % 4 * 32 >> 4)), kS, e > 0);
+        mma_commit(&sh.s_full[w][i]);
+      }
+      __syncwarp();
+    };
+    auto values = [&](int w, int i, int x, bool add) {  // half w has put P in S's place
+      ok = ok && bar_wait_all(&sh, &sh.p_full[w][i], p_phase >> (2 * w + i) & 1, p.status);
+      p_phase ^= 1u << (2 * w + i);
+      if (!ok) return;
+      tc_after();
+      const uint32_t v = v_low + x * (tc_tile<D>() >> 4);
+      if (elect_one()) {
+#pragma unroll
+        for (int e = 0; e < kTcKeys / 16; ++e)
+          mma_ts(o_of(w), s_of(w, i) + e * 8, tc_desc(v + e * (2048 >> 4)), kO, add || e > 0);
+        mma_commit(&sh.o_full[w]);
+      }
+      __syncwarp();
+    };
+    auto release = [&](int x) {
+      if (elect_one()) mma_commit(&sh.empty[x]);
+      __syncwarp();
+    };
+    for (long long t0 = t_begin; ok && t0 < t_end;) {
+      const int item = (int)(t0 / line.tiles), first = (int)(t0 % line.tiles);
+      const int n = (int)min(t_end - t0, (long long)(line.tiles - first));
+      t0 += n;
+      const int row0 = item % p.tc_groups * p.tc_rows;
+      const bool two = pair && row0 + kTcRows < R;  // the second half has rows
+      for (int w = 0; w < 2; ++w)  // the halves that have tiles here
+        if (w == 0 || (pair ? two : n > 1)) {
+          ok = ok && bar_wait_all(&sh, &sh.q_full[w], q_phase >> w & 1, p.status);
+          q_phase ^= 1u << w;
+        }
+      if (!ok) break;
+      // tile j belongs to both halves (pair), its S to buffer j & 1; or to
+      // half j & 1, its S to buffer j >> 1 & 1
+      for (int j = 0; ok && j < min(dist, n); ++j) {
+        const int k = take();
+        if (!ok) break;
+        scores(pair ? 0 : j & 1, pair ? j & 1 : j >> 1, k);
+        if (two) scores(1, j & 1, k);
+        release(k);
+      }
+      for (int j = 0; ok && j < n; ++j) {
+        const int v = take();
+        if (!ok) break;
+        const int w = pair ? 0 : j & 1, i = pair ? j & 1 : j >> 1 & 1;
+        const bool more = j + dist < n;
+        values(w, i, v, pair ? j > 0 : j > 1);
+        int k = 0;
+        if (more) k = take();
+        if (!ok) break;
+        if (more) scores(w, i, k);
+        if (two) values(1, i, v, j > 0);
+        if (!ok) break;
+        release(v);
+        if (more) {
+          if (two) scores(1, i, k);
+          release(k);
         }
       }
     }
-    __syncwarp();
+    if (!ok) {  // given up: the instructions in flight end before tensor memory goes
+      if (elect_one()) mma_commit(&sh.drain);
+      __syncwarp();
+      for (int i = 0; i < 100000 && !__all_sync(0xffffffffu, bar_try(&sh.drain, 0)); ++i) {
+      }
+    }
   } else if (warp < 8) {
     // ---------------- softmax: row r of half w
     const int w = warp >> 2, r = (warp & 3) * 32 + lane;
     const uint32_t lanes = (uint32_t)(warp & 3) << 21;  // this warp's 32 lanes of tensor memory
-    uint32_t s_phase = 0, o_phase = 0;
+    uint32_t s_phase = 0;  // bit i
+    int done = 0;          // tiles of this half so far
     bool ok = true;
     for (long long t0 = t_begin; ok && t0 < t_end;) {
       const int item = (int)(t0 / line.tiles), first = (int)(t0 % line.tiles);
@@ -872,7 +882,6 @@ __global__ void __launch_bounds__(kTcThreads, 1) tc_kernel(const AttnDev p) {
       t0 += n;
       const int row = item % p.tc_groups * p.tc_rows + (pair ? w * kTcRows : 0) + r;
       const bool live = row < R, any_live = row - lane < R, half_live = row - r < R;
-      float m = -INFINITY, l = 0.f;
       const int step = pair ? 1 : 2, j0 = pair ? 0 : w;
       const bool some = half_live && j0 < n;  // this half has tiles
       if (some) {
@@ -882,7 +891,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) tc_kernel(const AttnDev p) {
           const int rh = kv * p.G + row % p.G, rt = row / p.G % p.T, rb = row / p.G / p.T;
           qp = p.q + rb * p.q_bs + rt * p.q_ts + rh * p.q_hs;
         }
-#pragma unroll
+#pragma unroll 8
         for (int i = 0; i < D / 8; ++i) {
           uint4 x = make_uint4(0, 0, 0, 0);
           if (live) {
@@ -892,103 +901,83 @@ __global__ void __launch_bounds__(kTcThreads, 1) tc_kernel(const AttnDev p) {
             x.z ^= p.flip;
             x.w ^= p.flip;
           }
-          *reinterpret_cast<uint4 *>(sm + w * tc_tile<D>() + tc_at(r, i)) = x;
+          *reinterpret_cast<uint4 *>(sm + w * (kTcRows * D * 2) + tc_at(kTcRows, r, i)) = x;
         }
         fence_smem_async();
         __syncwarp();
         if (lane == 0) bar_arrive(&sh.q_full[w]);
       }
-      for (int j = j0; some && j < n; j += step) {
-        ok = bar_wait(&sh, &sh.s_full[w], s_phase, p.status);
-        ok = __all_sync(0xffffffffu, ok);
-        s_phase ^= 1;
+      float m = -INFINITY, l = 0.f;
+      int i = 0;  // which S
+      for (int j = j0; some && j < n; j += step, i ^= 1) {
+        ok = bar_wait_all(&sh, &sh.s_full[w][i], s_phase >> i & 1, p.status);
+        s_phase ^= 1u << i;
         if (!ok) break;
         tc_after();
         if (any_live) {
-          const int valid = min(kTcKeys, line.prefix - (first + j) * kTcKeys);
-          const uint32_t s = s_of(w) + lanes;
-          // S is read twice, 32 columns at a time, each read begun while the
-          // columns before it are worked on
+          const int valid = line.prefix - (first + j) * kTcKeys;
+          const uint32_t s = s_of(w, i) + lanes;
           uint32_t x[2][32];
-          float top = -INFINITY;
           tm_ld32(s, x[0]);
+          tm_ld32(s + 32, x[1]);
+          tm_wait_ld();
+          if (valid < kTcKeys) {
 #pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            tm_wait_ld();
-            tm_ld32(s + (q + 1) % 4 * 32, x[(q + 1) & 1]);
-            const uint32_t(&y)[32] = x[q & 1];
-            if (valid >= kTcKeys) {
-              float t[4] = {top, top, top, top};
-#pragma unroll
-              for (int i = 0; i < 32; ++i) t[i & 3] = fmaxf(t[i & 3], __uint_as_float(y[i]));
-              top = fmaxf(fmaxf(t[0], t[1]), fmaxf(t[2], t[3]));
-            } else {
-#pragma unroll
-              for (int i = 0; i < 32; ++i) top = q * 32 + i < valid ? fmaxf(top, __uint_as_float(y[i])) : top;
-            }
+            for (int e = 0; e < kTcKeys; ++e)
+              if (e >= valid) x[e / 32][e % 32] = 0xff800000u;  // -infinity
           }
+          float t[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+          for (int e = 0; e < kTcKeys; ++e) t[e & 3] = fmaxf(t[e & 3], __uint_as_float(x[e / 32][e % 32]));
+          float top = fmaxf(fmaxf(t[0], t[1]), fmaxf(t[2], t[3]));
           top = top == -INFINITY ? top : top * p.scale2;
           if (j == j0) {
             m = top;
           } else {
             const bool grow = top > m + kTcGrow;
             if (__any_sync(0xffffffffu, grow)) {
-              // (the last P V is complete: S came after it)
+              // O can be changed once the half's P V so far are complete
+              ok = bar_wait_all(&sh, &sh.o_full[w], (done - 1) & 1, p.status);
+              if (!ok) break;
+              tc_after();
               const float f = grow ? exp2_(m - top) : 1.f;
               if (grow) m = top;
               l *= f;
-              tm_wait_ld();  // (x[0]: the first columns, read again)
-              for (int q = 0; q < D / 32; ++q) {
-                tm_ld32(o_of(w) + lanes + q * 32, x[1]);
+              for (int q = 0; q < D / 16; ++q) {
+                uint32_t y[16];
+                tm_ld16(o_of(w) + lanes + q * 16, y);
                 tm_wait_ld();
 #pragma unroll
-                for (int i = 0; i < 32; ++i) x[1][i] = __float_as_uint(__uint_as_float(x[1][i]) * f);
-                tm_st32(o_of(w) + lanes + q * 32, x[1]);
+                for (int e = 0; e < 16; ++e) y[e] = __float_as_uint(__uint_as_float(y[e]) * f);
+                tm_st16(o_of(w) + lanes + q * 16, y);
               }
             }
           }
           const float b = m == -INFINITY ? 0.f : m;
           const unsigned long long scale = pack2(p.scale2, p.scale2), minus = pack2(-b, -b);
           unsigned long long sum = 0ull;
+          uint32_t h[32];
 #pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            tm_wait_ld();
-            if (q < 3) tm_ld32(s + (q + 1) * 32, x[(q + 1) & 1]);
-            const uint32_t(&y)[32] = x[q & 1];
-            uint32_t h[16];
-            if (valid >= kTcKeys) {
-#pragma unroll
-              for (int i = 0; i < 32; i += 2) {
-                const float2 t = unpack2(fma2(pack2(__uint_as_float(y[i]), __uint_as_float(y[i + 1])), scale, minus));
-                const float e0 = exp2_(t.x), e1 = exp2_(t.y);
-                sum = add2(sum, pack2(e0, e1));
-                h[i / 2] = Num<T>::pack(e0, e1);
-              }
-            } else {
-#pragma unroll
-              for (int i = 0; i < 32; i += 2) {
-                const float e0 = q * 32 + i < valid ? exp2_(fmaf(__uint_as_float(y[i]), p.scale2, -b)) : 0.f;
-                const float e1 = q * 32 + i + 1 < valid ? exp2_(fmaf(__uint_as_float(y[i + 1]), p.scale2, -b)) : 0.f;
-                sum = add2(sum, pack2(e0, e1));
-                h[i / 2] = Num<T>::pack(e0, e1);
-              }
-            }
-            tm_st16(s + q * 16, h);
+          for (int e = 0; e < kTcKeys; e += 2) {
+            const float2 y = unpack2(fma2(pack2(__uint_as_float(x[e / 32][e % 32]), __uint_as_float(x[e / 32][e % 32 + 1])), scale, minus));
+            const float e0 = exp2_(y.x), e1 = exp2_(y.y);
+            sum = add2(sum, pack2(e0, e1));
+            h[e / 2] = Num<T>::pack(e0, e1);
           }
+          tm_st32(s, h);
           const float2 both = unpack2(sum);
           l += both.x + both.y;
           tm_wait_st();
         }
         tc_before();
         __syncwarp();
-        if (lane == 0) bar_arrive(&sh.p_full[w]);
+        if (lane == 0) bar_arrive(&sh.p_full[w][i]);
+        ++done;
       }
       if (!ok) break;
       // ---- the partial result
       if (some) {
-        ok = bar_wait(&sh, &sh.o_full[w], o_phase, p.status);
-        ok = __all_sync(0xffffffffu, ok);
-        o_phase ^= 1;
+        ok = bar_wait_all(&sh, &sh.o_full[w], (done - 1) & 1, p.status);
         if (!ok) break;
         tc_after();
       }
@@ -1246,7 +1235,8 @@ extern "C" int mk_attn_shared(const mk_attn_shared_args *a, void *workspace, voi
   d.page_shift = (a->page & (a->page - 1)) == 0 ? __builtin_ctz((unsigned)a->page) : -1;
   d.n_prefix_pages = a->n_prefix_pages;
   d.table_width = a->table_width;
-  d.scale2 = (float)(std::fabs((double)a->scale) * 1.4426950408889634);
+  // (never 0, so that a masked score stays -infinity)
+  d.scale2 = std::max(1e-37f, (float)(std::fabs((double)a->scale) * 1.4426950408889634));
   d.flip = a->scale < 0.f ? 0x80008000u : 0u;
   int sms = 0;
   if ((rc = sm_count(&sms))) return rc;

@@ -41,7 +41,7 @@ struct AttnDev {
   float scale2;  // |scale| * log2(e): scores in powers of two
   uint32_t flip; // sign bits of two elements of q: set for a negative scale
   int n_prefix_items, own_tiles, n_items;  // items: prefix [kv head][row tile], then own [b][kv head][row tile]
-  float *part_o;    // [slot][kRows][d]
+  float4 *part_o;   // [slot][d / 4][kRows]
   float2 *part_ml;  // [slot][kRows]
   // the prefix on the tensor cores (tc_rows > 0; n_prefix_items is 0 then):
   // items [kv head][group of tc_rows rows]
@@ -49,6 +49,15 @@ struct AttnDev {
   float4 *tc_o;    // [slot][half][d / 4][kTcRows]
   float2 *tc_ml;   // [slot][half][kTcRows]
 };
+
+// floor(x / d) for 0 <= x < 2^52, 0 < d, with inv = 1 / d: a 64-bit division
+// costs about a hundred instructions in every thread's way.
+__device__ __forceinline__ long long quotient(long long x, long long d, double inv) {
+  long long q = (long long)((double)x * inv);
+  if (q * d > x) --q;
+  if ((q + 1) * d <= x) ++q;
+  return q;
+}
 
 // The work as a line of K/V tiles: item i owns tiles [start(i), start(i + 1));
 // block c of N takes the c-th equal share of the line, so every block reads
@@ -59,6 +68,8 @@ struct Line {
   int prefix, prefix_tiles;  // positions and tiles of the prefix
   long long own0, total;     // where the own items begin, and the end
   long long N;               // blocks that share it, every one with a tile at least
+  // where the part of block c begins, c <= N
+  __device__ __forceinline__ long long begin(long long c) const { return quotient(c * total, N, 1.0 / (double)N); }
 };
 
 // positions of sequence b (negative: unused), cut to its pages
@@ -214,15 +225,17 @@ __device__ __forceinline__ uint32_t at(int r, int c) {
   return (uint32_t)(r * (D * 2) + ((c ^ (r & 7)) << 4));
 }
 
-// Where a position's row is: byte offset into K or V of the row's head 0.
-__device__ __forceinline__ long long row_offset(const AttnDev &p, const int *list, int pos) {
-  const int pi = p.page_shift >= 0 ? pos >> p.page_shift : pos / p.page;
-  int pg = list[pi];
+// Where a position's row is, given its page: byte offset into K or V of the
+// row's head 0.
+__device__ __forceinline__ int page_index(const AttnDev &p, int pos) {
+  return p.page_shift >= 0 ? pos >> p.page_shift : pos / p.page;
+}
+__device__ __forceinline__ long long row_offset(const AttnDev &p, int pos, int pg) {
   if ((unsigned)pg >= (unsigned)p.n_pages) {
     report(p.status, MK_ERR_DEVICE_INPUT);
     pg = 0;
   }
-  return pg * p.kv_ps + (pos - pi * p.page) * p.kv_rs;
+  return pg * p.kv_ps + (pos - page_index(p, pos) * p.page) * p.kv_rs;
 }
 
 // The warps of a block work on their own: warp w copies, and attends over, the
@@ -239,14 +252,12 @@ __global__ void __launch_bounds__(kWarps * 32, kBlocksPerSm) part_kernel(const A
   constexpr int kHalf = kRows * D * 2, kStage = 2 * kHalf;  // bytes of a warp's 16 rows of K; of K and V
   char *const mine = sm + warp * kStages * kStage;
   const uint32_t mine_a = smem_addr(mine);
-  // Behind the tensor-core kernel this one starts as blocks of that one end;
-  // it reads nothing of its, and only waits for it before it ends itself.
-  if (!p.tc_rows) pdl_wait();
+  pdl_wait();
   pdl_trigger();
   const Line line = make_line(p, gridDim.x, sum, red);
   const long long c = blockIdx.x;
-  long long t0 = c < line.N ? c * line.total / line.N : 0;
-  const long long t_end = c < line.N ? (c + 1) * line.total / line.N : 0;
+  long long t0 = c < line.N ? line.begin(c) : 0;
+  const long long t_end = c < line.N ? line.begin(c + 1) : 0;
 
   while (t0 < t_end) {
     // ---- which item, and which of its tiles
@@ -254,7 +265,7 @@ __global__ void __launch_bounds__(kWarps * 32, kBlocksPerSm) part_kernel(const A
     int b = -1;                          // own item's sequence
     long long item_t0, item_t1;
     if (t0 < line.own0) {
-      item = (int)(t0 / line.prefix_tiles);
+      item = (int)quotient(t0, line.prefix_tiles, 1.0 / line.prefix_tiles);
       item_t0 = (long long)item * line.prefix_tiles;
       item_t1 = item_t0 + line.prefix_tiles;
       const int tiles = p.n_prefix_items / p.nkv;
@@ -265,7 +276,7 @@ __global__ void __launch_bounds__(kWarps * 32, kBlocksPerSm) part_kernel(const A
       hi = line.prefix;
     } else {
       const int per = p.nkv * p.own_tiles;
-      const int y = (int)((t0 - line.own0) / per);  // sum[b] <= y < sum[b + 1]
+      const int y = (int)quotient(t0 - line.own0, per, 1.0 / per);  // sum[b] <= y < sum[b + 1]
       int x0 = 0, x1 = p.B;
       while (x1 - x0 > 1) {
         const int mid = (x0 + x1) / 2;
@@ -275,7 +286,7 @@ __global__ void __launch_bounds__(kWarps * 32, kBlocksPerSm) part_kernel(const A
       b = x0;
       const int nt = sum[b + 1] - sum[b];
       const long long base = line.own0 + (long long)sum[b] * per;
-      const int k = (int)(t0 - base) / nt;
+      const int k = (int)quotient(t0 - base, nt, 1.0 / nt);
       item = p.n_prefix_items + b * per + k;
       item_t0 = base + (long long)k * nt;
       item_t1 = item_t0 + nt;
@@ -290,11 +301,12 @@ __global__ void __launch_bounds__(kWarps * 32, kBlocksPerSm) part_kernel(const A
 
     const int *table = p.table + (long long)b * p.table_width;  // (not used by prefix items)
     const int key0 = lo + first * kKeys + warp * 16;  // this warp's first position
-    auto look_up = [&](int i) {  // where this lane's position of tile i is (lanes 16-31: as 0-15)
+    auto look_up = [&](int i) {  // the page of this lane's position of tile i (lanes 16-31: as 0-15)
       const int pos = key0 + i * kKeys + (lane & 15);
-      return i < n_tiles && pos < hi ? row_offset(p, pos < line.prefix ? p.prefix_pages : table, pos) : 0ll;
+      return i < n_tiles && pos < hi ? (pos < line.prefix ? p.prefix_pages : table)[page_index(p, pos)] : 0;
     };
-    auto load = [&](int i, long long off) {  // tile i into stage i % kStages
+    auto load = [&](int i, int pg) {  // tile i into stage i % kStages
+      const long long off = row_offset(p, key0 + i * kKeys + (lane & 15), pg);
       const uint32_t dst = mine_a + (i % kStages) * kStage;
       constexpr int kChunks = D / 8, kPass = 32 / kChunks;  // rows of one instruction
       const int ch = lane % kChunks, r0 = lane / kChunks, left = hi - (key0 + i * kKeys);
@@ -307,14 +319,15 @@ __global__ void __launch_bounds__(kWarps * 32, kBlocksPerSm) part_kernel(const A
         cp16(dst + kHalf + at<D>(r, ch), p.v + o, live);
       }
     };
-    long long off = look_up(0);
+    int pg[kStages];  // pages of the tiles to come
+#pragma unroll
+    for (int i = 0; i < kStages; ++i) pg[i] = look_up(i);
 #pragma unroll
     for (int i = 0; i < kStages - 1; ++i) {
-      const long long next = look_up(i + 1);
-      if (i < n_tiles) load(i, off);
+      if (i < n_tiles) load(i, pg[i]);
       cp_commit();
-      off = next;
     }
+    int ahead = pg[kStages - 1];
 
     // ---- this thread's rows: r and r + 8 of the tile (g = lane / 4)
     auto row_of = [&](int r, int &rb, int &rt, int &rh) {
@@ -351,12 +364,12 @@ __global__ void __launch_bounds__(kWarps * 32, kBlocksPerSm) part_kernel(const A
     for (int i = 0; i < D / 8; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
 
     for (int i = 0; i < n_tiles; ++i) {
-      const long long next = look_up(i + kStages);
+      const int next = look_up(i + kStages);
       cp_wait<kStages - 2>();
       __syncwarp();
-      if (i + kStages - 1 < n_tiles) load(i + kStages - 1, off);
+      if (i + kStages - 1 < n_tiles) load(i + kStages - 1, ahead);
       cp_commit();
-      off = next;
+      ahead = next;
       const int pos0 = key0 + i * kKeys;
       if (pos0 >= hi) continue;
       const char *kt = mine + (i % kStages) * kStage, *vt = kt + kHalf;
@@ -469,17 +482,18 @@ __global__ void __launch_bounds__(kWarps * 32, kBlocksPerSm) part_kernel(const A
         l_s[warp][lane / 4 + 8 * h] = l[h];
       }
     }
-    float *po = reinterpret_cast<float *>(sm);  // [warp][row][D]
+    float *po = reinterpret_cast<float *>(sm);  // [warp][row][D + 4]
 #pragma unroll
     for (int d = 0; d < D / 8; ++d)
 #pragma unroll
       for (int h = 0; h < 2; ++h)
-        *reinterpret_cast<float2 *>(po + (warp * kRows + lane / 4 + 8 * h) * D + d * 8 + (lane & 3) * 2) =
+        *reinterpret_cast<float2 *>(po + (warp * kRows + lane / 4 + 8 * h) * (D + 4) + d * 8 + (lane & 3) * 2) =
             make_float2(o[d][2 * h], o[d][2 * h + 1]);
     __syncthreads();
     const long long slot = c + item;
-    for (int x = tid; x < n_rows * (D / 4); x += kWarps * 32) {
-      const int r = x / (D / 4), d = x % (D / 4) * 4;
+    for (int x = tid; x < kRows * (D / 4); x += kWarps * 32) {
+      const int r = x % kRows, d = x / kRows;
+      if (r >= n_rows) continue;
       float M = -INFINITY;
 #pragma unroll
       for (int w = 0; w < kWarps; ++w) M = fmaxf(M, m_s[w][r]);
@@ -489,19 +503,18 @@ __global__ void __launch_bounds__(kWarps * 32, kBlocksPerSm) part_kernel(const A
 #pragma unroll
       for (int w = 0; w < kWarps; ++w) {
         const float f = exp2_(m_s[w][r] - base);
-        const float4 y = *reinterpret_cast<const float4 *>(po + (w * kRows + r) * D + d);
+        const float4 y = *reinterpret_cast<const float4 *>(po + (w * kRows + r) * (D + 4) + d * 4);
         a.x += f * y.x;
         a.y += f * y.y;
         a.z += f * y.z;
         a.w += f * y.w;
         L += f * l_s[w][r];
       }
-      *reinterpret_cast<float4 *>(p.part_o + (slot * kRows + r) * D + d) = a;
+      p.part_o[(slot * (D / 4) + d) * kRows + r] = a;
       if (d == 0) p.part_ml[slot * kRows + r] = make_float2(M, L);
     }
     __syncthreads();  // before the next item's tiles
   }
-  if (p.tc_rows) pdl_wait();
 }
 
 // ---------------------------------------------------------------- the prefix on the tensor cores
@@ -513,8 +526,9 @@ __global__ void __launch_bounds__(kWarps * 32, kBlocksPerSm) part_kernel(const A
 //   tc_rows = 128: both take the same rows, and every other K/V tile.
 // Each half has two S of 64 positions: the tensor cores fill one while the
 // softmax works on the other.  Four warps copy the K/V tiles (16 bytes a time,
-// rows from the page list) into a ring in the order they are needed, and one
-// thread issues the matrix instructions.
+// rows from the page list) into a ring in the order they are needed, and a
+// warp for each half issues its matrix instructions (one warp for both spent
+// longer on the waits and descriptors than the instructions took).
 // P takes S's place in tensor memory, rounded to the operands' type: half a
 // step (2^-8 or 2^-11) of each weight, as the output's own rounding.
 // A row's maximum only moves when it grows by more than 2^8: until then the
@@ -523,7 +537,7 @@ __global__ void __launch_bounds__(kWarps * 32, kBlocksPerSm) part_kernel(const A
 
 constexpr int kTcRows = 128;  // rows of a half
 constexpr int kTcKeys = 64;   // positions of a tile
-constexpr int kTcThreads = 13 * 32;  // warps 0-3 and 4-7: softmax; 8-11: copies; 12: matrix instructions
+constexpr int kTcThreads = 14 * 32;  // warps 0-3 and 4-7: softmax; 8-11: copies; 12 and 13: matrix instructions
 constexpr float kTcGrow = 8.f;
 template <int D>
 constexpr int tc_tile() {
@@ -636,7 +650,7 @@ __device__ __forceinline__ bool bar_try(uint64_t *b, uint32_t parity) {
 
 struct TcShared {
   uint64_t full[16], empty[16];  // ring entries
-  uint64_t q_full[2], s_full[2][2], p_full[2][2], o_full[2], drain;  // [half][which S]; o_full: a P V is complete
+  uint64_t q_full[2], s_full[2][2], p_full[2][2], o_full[2], drain[2];  // [half][which S]; o_full: a P V is complete
   uint32_t tmem;
   volatile int dead;  // a wait gave up
 };
@@ -669,10 +683,30 @@ __device__ __forceinline__ void cp_arrive(uint64_t *b) {
   asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_addr(b)) : "memory");
 }
 
+// The order in which the n tiles of an item pass through the ring: K of the
+// first `ahead`, then V j and K j + ahead in turn, then the other V.
+struct TcOrder {
+  int n, ahead;
+  __device__ __forceinline__ int k_at(int j) const { return j < ahead ? j : 2 * j - ahead + 1; }
+  __device__ __forceinline__ int v_at(int j) const { return j < n - ahead ? ahead + 2 * j : n + j; }
+  __device__ __forceinline__ int tile(int e, bool &is_v) const {  // of entry e
+    is_v = e >= ahead && (e >= 2 * n - ahead || !((e - ahead) & 1));
+    return !is_v ? (e < ahead ? e : (e + ahead - 1) / 2) : e < 2 * n - ahead ? (e - ahead) / 2 : e - n;
+  }
+};
+
 // The blocks' line of tiles, as for the other items.
 struct TcLine {
   int prefix, tiles, n_items;
   long long total, N;
+  double inv_tiles;
+  __device__ __forceinline__ long long begin(long long c) const { return quotient(c * total, N, 1.0 / (double)N); }
+  // the item that tile t is of, and which of its tiles it is
+  __device__ __forceinline__ int item_of(long long t, int &first) const {
+    const int i = (int)quotient(t, tiles, inv_tiles);
+    first = (int)(t - (long long)i * tiles);
+    return i;
+  }
 };
 __device__ __forceinline__ TcLine tc_line(const AttnDev &p, int prefix, int blocks) {
   TcLine l;
@@ -681,6 +715,7 @@ __device__ __forceinline__ TcLine tc_line(const AttnDev &p, int prefix, int bloc
   l.n_items = p.nkv * p.tc_groups;
   l.total = (long long)l.tiles * l.n_items;
   l.N = min((long long)blocks, l.total);
+  l.inv_tiles = l.tiles > 0 ? 1.0 / l.tiles : 0.0;
   return l;
 }
 
@@ -693,10 +728,11 @@ __global__ void __launch_bounds__(kTcThreads, 1) tc_kernel(const AttnDev p) {
   const uint32_t base = (smem_addr(sm_raw) + 1023) & ~1023u;
   char *sm = sm_raw + (base - smem_addr(sm_raw));
   const uint32_t ring = base + 2 * kTcRows * D * 2;
+  const bool pair = p.tc_rows == 2 * kTcRows;  // the halves have rows of their own
   if (tid == 0) {
     for (int i = 0; i < kRing; ++i) {
       bar_init(&sh.full[i], 128);
-      bar_init(&sh.empty[i], 1);
+      bar_init(&sh.empty[i], pair ? 2 : 1);
     }
     for (int w = 0; w < 2; ++w) {
       bar_init(&sh.q_full[w], 4);
@@ -706,13 +742,15 @@ __global__ void __launch_bounds__(kTcThreads, 1) tc_kernel(const AttnDev p) {
       }
       bar_init(&sh.o_full[w], 1);
     }
-    bar_init(&sh.drain, 1);
+    bar_init(&sh.drain[0], 1);
+    bar_init(&sh.drain[1], 1);
     sh.dead = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
   if (warp == 12)
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_addr(&sh.tmem)) : "memory");
-  pdl_wait();
+  // This kernel starts as blocks of the own parts' kernel end.  It reads
+  // nothing of theirs, and only waits for them before it ends itself.
   pdl_trigger();
   tc_before();
   __syncthreads();
@@ -720,46 +758,44 @@ __global__ void __launch_bounds__(kTcThreads, 1) tc_kernel(const AttnDev p) {
   const uint32_t tm = sh.tmem;
   const TcLine line = tc_line(p, prefix_of(p), gridDim.x);
   const long long c = blockIdx.x;
-  const bool pair = p.tc_rows == 2 * kTcRows;  // the halves have rows of their own
   const int dist = pair ? 2 : 4;               // K tiles that are multiplied ahead of their V
   const int R = p.B * p.T * p.G;
-  const long long t_begin = c < line.N ? c * line.total / line.N : 0, t_end = c < line.N ? (c + 1) * line.total / line.N : 0;
+  const long long t_begin = c < line.N ? line.begin(c) : 0, t_end = c < line.N ? line.begin(c + 1) : 0;
   auto s_of = [&](int w, int i) { return tm + w * 128 + i * 64; };
   auto o_of = [&](int w) { return tm + 256 + w * D; };
 
   if (warp >= 8 && warp < 12) {
     // ---------------- copies: warp w of the four takes rows 16 w .. 16 w + 15
-    // of every tile; a lane looks up the page of one, an entry ahead
+    // of every tile; a lane looks up the page of one, three entries ahead
     int g = 0;  // ring entries begun
     bool ok = true;
     const int row = (warp - 8) * 16;
     for (long long t0 = t_begin; ok && t0 < t_end;) {
-      const int item = (int)(t0 / line.tiles), first = (int)(t0 % line.tiles);
+      int first;
+      const int item = line.item_of(t0, first);
       const int n = (int)min(t_end - t0, (long long)(line.tiles - first)), kv = item / p.tc_groups;
       t0 += n;
-      // the order of use: K 0 .. dist - 1, then V j, K j + dist
-      const int ahead = min(dist, n);
-      auto tile_of = [&](int e) {  // entry e's tile; V: + 2^30
-        if (e < ahead) return e;
-        e -= ahead;
-        const int both = 2 * (n - ahead);
-        return e < both ? (e & 1 ? e / 2 + ahead : e / 2 + (1 << 30)) : e - (n - ahead) + (1 << 30);
-      };
+      const TcOrder order{n, min(dist, n)};
       auto look_up = [&](int e) {
-        const int pos = (first + (tile_of(e) & ~(1 << 30))) * kTcKeys + row + (lane & 15);
-        return e < 2 * n && pos < line.prefix ? row_offset(p, p.prefix_pages, pos) : 0ll;
+        bool v;
+        const int pos = (first + order.tile(e, v)) * kTcKeys + row + (lane & 15);
+        return e < 2 * n && pos < line.prefix ? p.prefix_pages[page_index(p, pos)] : 0;
       };
-      long long next = look_up(0);
+      int pg0 = look_up(0), pg1 = look_up(1), pg2 = look_up(2);
       for (int e = 0; e < 2 * n; ++e) {
-        const long long off = next;
-        next = look_up(e + 1);
-        const int slot = g % kRing, j = tile_of(e);
+        const int pg = pg0;
+        pg0 = pg1;
+        pg1 = pg2;
+        pg2 = look_up(e + 3);
+        bool is_v;
+        const int slot = g % kRing, j = order.tile(e, is_v);
         if (g >= kRing) ok = bar_wait_all(&sh, &sh.empty[slot], ((g / kRing) & 1) ^ 1, p.status);
         if (!ok) break;
         const uint32_t dst = ring + slot * tc_tile<D>();
         constexpr int kChunks = D / 8, kPass = 32 / kChunks;
-        const int ch = lane % kChunks, r0 = lane / kChunks, left = line.prefix - (first + (j & ~(1 << 30))) * kTcKeys - row;
-        const char *from = (j >> 30 ? p.v : p.k) + kv * p.kv_hs + ch * 16;
+        const int ch = lane % kChunks, r0 = lane / kChunks, left = line.prefix - (first + j) * kTcKeys - row;
+        const char *from = (is_v ? p.v : p.k) + kv * p.kv_hs + ch * 16;
+        const long long off = row_offset(p, (first + j) * kTcKeys + row + (lane & 15), pg);
 #pragma unroll
         for (int x = 0; x < 16 / kPass; ++x) {
           const int r = x * kPass + r0;
@@ -772,101 +808,88 @@ __global__ void __launch_bounds__(kTcThreads, 1) tc_kernel(const AttnDev p) {
     }
     cp_commit();
     cp_wait<0>();
-  } else if (warp == 12) {
-    // ---------------- matrix instructions: the warp walks as one, an elected
-    // lane issues
+  } else if (warp >= 12) {
+    // ---------------- matrix instructions of half w: the warp walks as one, an
+    // elected lane issues
     constexpr uint32_t kType = std::is_same<T, __nv_bfloat16>::value ? 1u : 0u;
     // 32-bit accumulators, both operands of this type, 128 rows; N = 64 positions, or N = D with V's
     // leading dimension the other way round
     constexpr uint32_t kS = (1u << 4) | (kType << 7) | (kType << 10) | ((kTcKeys / 8u) << 17) | ((128u / 16) << 24);
     constexpr uint32_t kO = (1u << 4) | (kType << 7) | (kType << 10) | (1u << 16) | ((uint32_t)(D / 8) << 17) | ((128u / 16) << 24);
-    const uint32_t q_low = tc_low(base, 16), k_low = tc_low(ring, 16), v_low = tc_low(ring, kTcKeys * 128);
-    int slot = 0;                       // of the ring
-    uint32_t full_phase = 0, q_phase = 0, p_phase = 0;  // one bit; bit w; bit 2 w + i
+    const int w = warp - 12;
+    const uint32_t q_low = tc_low(base, 16) + w * (kTcRows * D * 2 >> 4);
+    const uint32_t k_low = tc_low(ring, 16), v_low = tc_low(ring, kTcKeys * 128);
+    int g = 0;                          // ring entries before this item
+    uint32_t q_phase = 0, p_phase = 0;  // one bit; bit i
     bool ok = true;
-    auto take = [&]() {  // the next ring entry's tile
-      const int x = slot;
-      ok = ok && bar_wait_all(&sh, &sh.full[x], full_phase, p.status);
+    auto take = [&](int e) {  // entry e's tile has landed
+      const int x = (g + e) % kRing;
+      ok = ok && bar_wait_all(&sh, &sh.full[x], ((g + e) / kRing) & 1, p.status);
       fence_smem_async();  // the copies' writes, before the tensor cores' reads
-      if (++slot == kRing) {
-        slot = 0;
-        full_phase ^= 1;
-      }
       return x;
     };
-    auto scores = [&](int w, int i, int x) {
-      const uint32_t q = q_low + w * (kTcRows * D * 2 >> 4), k = k_low + x * (tc_tile<D>() >> 4);
+    auto scores = [&](int i, int x) {
+      const uint32_t k = k_low + x * (tc_tile<D>() >> 4);
       if (elect_one()) {
 #pragma unroll
         for (int e = 0; e < D / 16; ++e)
-          mma_ss(s_of(w, i), tc_desc(q + (e / 4 * (kTcRows * 128) + e % 4 * 32 >> 4)),
+          mma_ss(s_of(w, i), tc_desc(q_low + (e / 4 * (kTcRows * 128) + e % 4 * 32 >> 4)),
                  tc_desc(k + (e / 4 * (kTcKeys * 128) + e % 4 * 32 >> 4)), kS, e > 0);
         mma_commit(&sh.s_full[w][i]);
+        mma_commit(&sh.empty[x]);
       }
-      __syncwarp();
-    };
-    auto values = [&](int w, int i, int x, bool add) {  // half w has put P in S's place
-      ok = ok && bar_wait_all(&sh, &sh.p_full[w][i], p_phase >> (2 * w + i) & 1, p.status);
-      p_phase ^= 1u << (2 * w + i);
-      if (!ok) return;
-      tc_after();
-      const uint32_t v = v_low + x * (tc_tile<D>() >> 4);
-      if (elect_one()) {
-#pragma unroll
-        for (int e = 0; e < kTcKeys / 16; ++e)
-          mma_ts(o_of(w), s_of(w, i) + e * 8, tc_desc(v + e * (2048 >> 4)), kO, add || e > 0);
-        mma_commit(&sh.o_full[w]);
-      }
-      __syncwarp();
-    };
-    auto release = [&](int x) {
-      if (elect_one()) mma_commit(&sh.empty[x]);
       __syncwarp();
     };
     for (long long t0 = t_begin; ok && t0 < t_end;) {
-      const int item = (int)(t0 / line.tiles), first = (int)(t0 % line.tiles);
+      int first;
+      const int item = line.item_of(t0, first);
       const int n = (int)min(t_end - t0, (long long)(line.tiles - first));
       t0 += n;
-      const int row0 = item % p.tc_groups * p.tc_rows;
-      const bool two = pair && row0 + kTcRows < R;  // the second half has rows
-      for (int w = 0; w < 2; ++w)  // the halves that have tiles here
-        if (w == 0 || (pair ? two : n > 1)) {
-          ok = ok && bar_wait_all(&sh, &sh.q_full[w], q_phase >> w & 1, p.status);
-          q_phase ^= 1u << w;
+      const TcOrder order{n, min(dist, n)};
+      // this half's tiles: all (pair) or every other; its k-th S is in buffer k & 1
+      const int step = pair ? 1 : 2, j0 = pair ? 0 : w;
+      if (item % p.tc_groups * p.tc_rows + (pair ? w * kTcRows : 0) >= R) {
+        // no rows: the tiles only pass
+        for (int e = 0; ok && e < 2 * n; ++e) {
+          const int x = take(e);
+          if (ok && elect_one()) mma_commit(&sh.empty[x]);
+          __syncwarp();
         }
-      if (!ok) break;
-      // tile j belongs to both halves (pair), its S to buffer j & 1; or to
-      // half j & 1, its S to buffer j >> 1 & 1
-      for (int j = 0; ok && j < min(dist, n); ++j) {
-        const int k = take();
-        if (!ok) break;
-        scores(pair ? 0 : j & 1, pair ? j & 1 : j >> 1, k);
-        if (two) scores(1, j & 1, k);
-        release(k);
-      }
-      for (int j = 0; ok && j < n; ++j) {
-        const int v = take();
-        if (!ok) break;
-        const int w = pair ? 0 : j & 1, i = pair ? j & 1 : j >> 1 & 1;
-        const bool more = j + dist < n;
-        values(w, i, v, pair ? j > 0 : j > 1);
-        int k = 0;
-        if (more) k = take();
-        if (!ok) break;
-        if (more) scores(w, i, k);
-        if (two) values(1, i, v, j > 0);
-        if (!ok) break;
-        release(v);
-        if (more) {
-          if (two) scores(1, i, k);
-          release(k);
+      } else if (j0 < n) {
+        ok = ok && bar_wait_all(&sh, &sh.q_full[w], q_phase, p.status);
+        q_phase ^= 1;
+        for (int k = 0; ok && k < 2 && j0 + k * step < n; ++k) {
+          const int x = take(order.k_at(j0 + k * step));
+          if (ok) scores(k, x);
+        }
+        int i = 0;
+        for (int j = j0; ok && j < n; j += step, i ^= 1) {
+          const int v = take(order.v_at(j));
+          ok = ok && bar_wait_all(&sh, &sh.p_full[w][i], p_phase >> i & 1, p.status);  // P is in S's place
+          p_phase ^= 1u << i;
+          if (!ok) break;
+          tc_after();
+          const uint32_t low = v_low + v * (tc_tile<D>() >> 4);
+          if (elect_one()) {
+#pragma unroll
+            for (int e = 0; e < kTcKeys / 16; ++e)
+              mma_ts(o_of(w), s_of(w, i) + e * 8, tc_desc(low + e * (2048 >> 4)), kO, j > j0 || e > 0);
+            mma_commit(&sh.o_full[w]);
+            mma_commit(&sh.empty[v]);
+          }
+          __syncwarp();
+          if (j + 2 * step < n) {
+            const int x = take(order.k_at(j + 2 * step));
+            if (ok) scores(i, x);
+          }
         }
       }
+      g += 2 * n;
     }
     if (!ok) {  // given up: the instructions in flight end before tensor memory goes
-      if (elect_one()) mma_commit(&sh.drain);
+      if (elect_one()) mma_commit(&sh.drain[w]);
       __syncwarp();
-      for (int i = 0; i < 100000 && !__all_sync(0xffffffffu, bar_try(&sh.drain, 0)); ++i) {
+      for (int i = 0; i < 100000 && !__all_sync(0xffffffffu, bar_try(&sh.drain[w], 0)); ++i) {
       }
     }
   } else if (warp < 8) {
@@ -877,7 +900,8 @@ __global__ void __launch_bounds__(kTcThreads, 1) tc_kernel(const AttnDev p) {
     int done = 0;          // tiles of this half so far
     bool ok = true;
     for (long long t0 = t_begin; ok && t0 < t_end;) {
-      const int item = (int)(t0 / line.tiles), first = (int)(t0 % line.tiles);
+      int first;
+      const int item = line.item_of(t0, first);
       const int n = (int)min(t_end - t0, (long long)(line.tiles - first)), kv = item / p.tc_groups;
       t0 += n;
       const int row = item % p.tc_groups * p.tc_rows + (pair ? w * kTcRows : 0) + r;
@@ -983,24 +1007,27 @@ __global__ void __launch_bounds__(kTcThreads, 1) tc_kernel(const AttnDev p) {
       }
       if (any_live) {
         const long long slot = (c + item) * 2 + w;
-        if (some)
-          for (int q = 0; q < D / 32; ++q) {
-            uint32_t x[32];
+        for (int q = 0; q < D / 32; ++q) {
+          uint32_t x[32];
+          if (some) {
             tm_ld32(o_of(w) + lanes + q * 32, x);
             tm_wait_ld();
-            if (live)
-#pragma unroll
-              for (int i = 0; i < 8; ++i)
-                p.tc_o[(slot * (D / 4) + q * 8 + i) * kTcRows + r] =
-                    make_float4(__uint_as_float(x[4 * i]), __uint_as_float(x[4 * i + 1]), __uint_as_float(x[4 * i + 2]),
-                                __uint_as_float(x[4 * i + 3]));
           }
+          if (live)
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+              p.tc_o[(slot * (D / 4) + q * 8 + i) * kTcRows + r] =
+                  some ? make_float4(__uint_as_float(x[4 * i]), __uint_as_float(x[4 * i + 1]),
+                                     __uint_as_float(x[4 * i + 2]), __uint_as_float(x[4 * i + 3]))
+                       : make_float4(0.f, 0.f, 0.f, 0.f);
+        }
         if (live) p.tc_ml[slot * kTcRows + r] = make_float2(m, l);
       }
       tc_before();
     }
   }
   __syncthreads();
+  pdl_wait();
   if (warp == 12) {
     tc_after();
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
@@ -1008,110 +1035,148 @@ __global__ void __launch_bounds__(kTcThreads, 1) tc_kernel(const AttnDev p) {
   }
 }
 
-// Join the partials of every row: a warp per row.  The lanes look at the
-// partials' maxima and sums, a partial each; then each lane adds up four
-// elements (D = 64: each half of the warp every other partial).
+// Join the partials of every row.  A block takes kJoinRows rows of one K/V head
+// that follow one another in the partials, where a group of four elements of
+// all rows is contiguous: each load of a warp is 4 pieces of 128 bytes.  Of its
+// 16 warps, 4 share the elements and 4 the partials: lane q * 8 + i of warp
+// 4 s + w adds up, for row i, element groups w * D / 16 + q + 4 k of partials
+// s, s + 4, ...  The weights 2^(m - M) come first, into shared memory.
+constexpr int kJoinRows = 8;
+constexpr int kJoinThreads = 512;
+constexpr int kJoinMax = 512;  // partials of a row whose weights are kept at a time
 template <class T, int D>
-__global__ void __launch_bounds__(128) join_kernel(const AttnDev p, int N, int tc_n) {
+__global__ void __launch_bounds__(kJoinThreads) join_kernel(const AttnDev p, int N, int tc_n) {
   extern __shared__ int sum[];
-  __shared__ int red[4];
-  const int lane = threadIdx.x & 31;
+  __shared__ int red[kJoinThreads / 32];
+  __shared__ float w_s[kJoinMax][kJoinRows], m_s[kJoinThreads], l_s[kJoinThreads];
+  __shared__ float4 a_s[3][D / 4][kJoinRows];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, ri = lane % kJoinRows;
+  const int d0 = (warp & 3) * (D / 16) + lane / kJoinRows, part = warp >> 2;
+  constexpr int kGroups = D / 64;  // element groups of a lane
   pdl_wait();
   const Line line = make_line(p, N, sum, red);
   const TcLine tc = tc_line(p, p.tc_rows ? line.prefix : 0, tc_n);
-  const int rows = p.B * p.T * p.nq;
-  for (int x = blockIdx.x * 4 + (threadIdx.x >> 5); x < rows; x += gridDim.x * 4) {
-    const int h = x % p.nq, t = x / p.nq % p.T, b = x / p.nq / p.T;
-    if (p.lens[b] < 0) continue;
-    const int kv = h / p.G, g = h % p.G, pr = (b * p.T + t) * p.G + g;
-    // partials of this row: n_tc of the tensor cores, then n_pre and n_own of the other kernel
-    int n_tc = 0, n_pre = 0, n_own = 0, r_tc = 0, r_own = 0;
-    long long s_tc = 0, s_pre = 0, s_own = 0;
+  const double inv_own = line.total > 0 ? 1.0 / (double)line.total : 0.0, inv_tc = tc.total > 0 ? 1.0 / (double)tc.total : 0.0;
+  const int R = p.B * p.T * p.G, blocks = (R + kJoinRows - 1) / kJoinRows;
+  for (int x = blockIdx.x; x < blocks * p.nkv; x += gridDim.x) {
+    const int kv = x / blocks, first = x % blocks * kJoinRows, row = first + ri;
+    const int g = row % p.G, t = row / p.G % p.T, b = min(row / p.G / p.T, p.B - 1);
+    const bool live = row < R && p.lens[b] >= 0, shared = live && shares(p, b, line.prefix);
     // the block that owns tile t is the largest c with c * total / N <= t; with
     // N <= total every block between two that share an item has a part of it
-    auto span = [](long long t0, long long t1, long long n, long long total, long long item, long long &first) {
-      first = ((t0 + 1) * n - 1) / total + item;
-      return (int)((t1 * n - 1) / total + item - first) + 1;
+    auto span = [](long long t0, long long t1, long long n, long long total, double inv, int item, int &slot) {
+      const int c0 = (int)quotient((t0 + 1) * n - 1, total, inv), c1 = (int)quotient(t1 * n - 1, total, inv);
+      slot = c0 + item;
+      return c1 - c0 + 1;
     };
-    if (shares(p, b, line.prefix)) {
-      if (p.tc_rows) {
-        const long long item = kv * p.tc_groups + pr / p.tc_rows;
-        n_tc = span(item * tc.tiles, (item + 1) * tc.tiles, tc.N, tc.total, item, s_tc);
-        r_tc = pr % p.tc_rows;
-        if (p.tc_rows == kTcRows) n_tc *= 2;  // both halves hold a part of the row
+    // this row's partials: n1 of the prefix, n2 of its own part
+    int n1 = 0, n2 = 0, slot;
+    const float2 *ml1 = p.part_ml, *ml2 = p.part_ml;
+    const float4 *o1 = p.part_o, *o2 = p.part_o;
+    int ms1 = kRows, rows1 = kRows;
+    if (line.prefix > 0 && (p.tc_rows || p.n_prefix_items)) {
+      if (p.tc_rows) {  // (a block's rows are of one group: tc_rows is a multiple of kJoinRows)
+        const int item = kv * p.tc_groups + first / p.tc_rows, in = row % p.tc_rows, r = in % kTcRows;
+        n1 = span((long long)item * tc.tiles, (long long)(item + 1) * tc.tiles, tc.N, tc.total, inv_tc, item, slot);
+        const long long half = slot * 2ll + in / kTcRows;  // pair: this row's half of each slot; else both
+        ms1 = 2 * kTcRows;
+        if (p.tc_rows == kTcRows) n1 *= 2, ms1 = kTcRows;
+        rows1 = kTcRows;
+        ml1 = p.tc_ml + half * kTcRows + r;
+        o1 = p.tc_o + (half * (D / 4) + d0) * kTcRows + r;
       } else {
-        const int item = kv * (p.n_prefix_items / p.nkv) + pr / kRows;
-        n_pre = span((long long)item * line.prefix_tiles, (long long)(item + 1) * line.prefix_tiles, line.N, line.total, item, s_pre);
+        const int item = kv * (p.n_prefix_items / p.nkv) + first / kRows, r = row % kRows;
+        n1 = span((long long)item * line.prefix_tiles, (long long)(item + 1) * line.prefix_tiles, line.N, line.total, inv_own, item, slot);
+        ml1 = p.part_ml + (long long)slot * kRows + r;
+        o1 = p.part_o + ((long long)slot * (D / 4) + d0) * kRows + r;
       }
+      if (!shared) n1 = 0;
     }
     const int nt = sum[b + 1] - sum[b];
-    if (nt > 0) {
-      const int per = p.nkv * p.own_tiles, w = t * p.G + g, k = kv * p.own_tiles + w / kRows;
+    if (live && nt > 0) {
+      const int per = p.nkv * p.own_tiles, w = t * p.G + g, k = kv * p.own_tiles + w / kRows, r = w % kRows;
       const long long t0 = line.own0 + (long long)sum[b] * per + (long long)k * nt;
-      n_own = span(t0, t0 + nt, line.N, line.total, p.n_prefix_items + b * per + k, s_own);
-      r_own = w % kRows;
+      n2 = span(t0, t0 + nt, line.N, line.total, inv_own, p.n_prefix_items + b * per + k, slot);
+      ml2 = p.part_ml + (long long)slot * kRows + r;
+      o2 = p.part_o + ((long long)slot * (D / 4) + d0) * kRows + r;
     }
-    const int n = n_tc + n_pre + n_own;
-    auto tc_slot = [&](int i) {  // half-slot of the i-th
-      return p.tc_rows == kTcRows ? s_tc * 2 + i : (s_tc + i) * 2 + r_tc / kTcRows;
+    // ---- the row's maximum and sum: thread 8 k + i looks at partials k, k + 64, ... of row i
+    const int n = n1 + n2;
+    auto ml_of = [&](int i) {
+      const float2 *y = i < n1 ? ml1 + i * (long long)ms1 : ml2 + (i - n1) * (long long)kRows;
+      return *y;
     };
-    auto part_row = [&](int i) {
-      i -= n_tc;
-      return i < n_pre ? (s_pre + i) * kRows + pr % kRows : (s_own + i - n_pre) * kRows + r_own;
-    };
-    auto ml_of = [&](int i) { return i < n_tc ? p.tc_ml[tc_slot(i) * kTcRows + r_tc % kTcRows] : p.part_ml[part_row(i)]; };
-    constexpr int kWays = 128 / D;
-    const int d4 = lane % (D / 4), way = lane / (D / 4);
     float M = -INFINITY, L = 0.f;
-    float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int i0 = 0; i0 < n; i0 += 32) {  // 32 partials at a time, a lane looking at each
-      const int k = min(32, n - i0);
-      const float2 ml = lane < k ? ml_of(i0 + lane) : make_float2(-INFINITY, 0.f);
-      float top = ml.y != 0.f ? ml.x : -INFINITY;
+    for (int i = tid / kJoinRows; i < n; i += kJoinThreads / kJoinRows) {
+      const float2 y = ml_of(i);
+      const float m = y.y == 0.f ? -INFINITY : y.x, top = fmaxf(M, m), base = top == -INFINITY ? 0.f : top;
+      L = L * exp2_(M - base) + (y.y == 0.f ? 0.f : y.y * exp2_(m - base));
+      M = top;
+    }
+    auto meet = [&](float m, float l) {
+      const float top = fmaxf(M, m), base = top == -INFINITY ? 0.f : top;
+      L = L * exp2_(M - base) + l * exp2_(m - base);
+      M = top;
+    };
 #pragma unroll
-      for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-      const float old = M;
-      M = fmaxf(M, top);
-      const float base = M == -INFINITY ? 0.f : M, scale = exp2_(old - base);
-      // (a partial without a sum has nothing, and its o was not written)
-      const bool there = ml.y != 0.f;
-      const float f = there ? exp2_(ml.x - base) : 0.f;
-      const unsigned some = __ballot_sync(0xffffffffu, there);
-      L = L * scale + f * ml.y;
-      a.x *= scale;
-      a.y *= scale;
-      a.z *= scale;
-      a.w *= scale;
-      // (loads that wait for nothing: from the last partial where there is no other)
-      auto add = [&](int i, int end, const float4 &y) {
-        const float w = __shfl_sync(0xffffffffu, f, (i + way) & 31);
-        const bool use = i + way < end && (some >> ((i + way) & 31) & 1);
-        a.x += use ? w * y.x : 0.f;
-        a.y += use ? w * y.y : 0.f;
-        a.z += use ? w * y.z : 0.f;
-        a.w += use ? w * y.w : 0.f;
-      };
-      const int k_tc = max(0, min(k, n_tc - i0));
-#pragma unroll 8
-      for (int i = 0; i < k_tc; i += kWays)
-        add(i, k_tc, p.tc_o[(tc_slot(min(i0 + i + way, n_tc - 1)) * (D / 4) + d4) * kTcRows + r_tc % kTcRows]);
+    for (int o = 8; o < 32; o <<= 1) meet(__shfl_xor_sync(0xffffffffu, M, o), __shfl_xor_sync(0xffffffffu, L, o));
+    if (lane < kJoinRows) m_s[warp * kJoinRows + ri] = M, l_s[warp * kJoinRows + ri] = L;
+    __syncthreads();
+    M = -INFINITY, L = 0.f;
+    for (int w = 0; w < min(kJoinThreads / 32, (n + 3) / 4); ++w) meet(m_s[w * kJoinRows + ri], l_s[w * kJoinRows + ri]);
+    const float base = M == -INFINITY ? 0.f : M;
+    // ---- the elements
+    float4 a[kGroups];
+#pragma unroll
+    for (int k = 0; k < kGroups; ++k) a[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+    const int n_max = __reduce_max_sync(0xffffffffu, n);  // (of the block: every warp has the same rows)
+    for (int i0 = 0; i0 < n_max; i0 += kJoinMax) {
+      for (int i = i0 + tid / kJoinRows; i < min(n, i0 + kJoinMax); i += kJoinThreads / kJoinRows) {
+        const float2 y = ml_of(i);
+        w_s[i - i0][ri] = y.y == 0.f ? 0.f : exp2_(y.x - base);
+      }
+      __syncthreads();
+      auto add = [&](const float4 *o, long long os, int rows, int from, int to) {  // partials from, from + 4, ... of this row
 #pragma unroll 4
-      for (int i = k_tc; i < k; i += kWays)
-        add(i, k, *reinterpret_cast<const float4 *>(p.part_o + part_row(min(i0 + i + way, n - 1)) * D + d4 * 4));
+        for (int i = from; i < to; i += 4) {
+          const float f = w_s[i - i0][ri];
+#pragma unroll
+          for (int k = 0; k < kGroups; ++k) {
+            const float4 z = o[i * os + 4 * k * rows];
+            a[k].x = fmaf(z.x, f, a[k].x);
+            a[k].y = fmaf(z.y, f, a[k].y);
+            a[k].z = fmaf(z.z, f, a[k].z);
+            a[k].w = fmaf(z.w, f, a[k].w);
+          }
+        }
+      };
+      const int end = min(n, i0 + kJoinMax), cut = min(max(n1, i0), end), own = cut + ((part - cut) & 3);
+      add(o1, (long long)ms1 * (D / 4), rows1, i0 + part, cut);
+      add(o2 - (long long)n1 * kRows * (D / 4), (long long)kRows * (D / 4), kRows, own, end);
+      __syncthreads();
     }
 #pragma unroll
-    for (int o = 16; o; o >>= 1) L += __shfl_xor_sync(0xffffffffu, L, o);
-    if (kWays == 2) {
-      a.x += __shfl_xor_sync(0xffffffffu, a.x, 16);
-      a.y += __shfl_xor_sync(0xffffffffu, a.y, 16);
-      a.z += __shfl_xor_sync(0xffffffffu, a.z, 16);
-      a.w += __shfl_xor_sync(0xffffffffu, a.w, 16);
+    for (int k = 0; k < kGroups; ++k)
+      if (part > 0) a_s[part - 1][d0 + 4 * k][ri] = a[k];
+    __syncthreads();
+    if (part == 0 && live) {
+      const float inv = L == 0.f ? 0.f : 1.f / L;  // (a NaN stays)
+      char *op = p.out + b * p.o_bs + t * p.o_ts + (kv * p.G + g) * p.o_hs + d0 * 8;
+#pragma unroll
+      for (int k = 0; k < kGroups; ++k) {
+        for (int s = 0; s < 3; ++s) {
+          const float4 z = a_s[s][d0 + 4 * k][ri];
+          a[k].x += z.x;
+          a[k].y += z.y;
+          a[k].z += z.z;
+          a[k].w += z.w;
+        }
+        *reinterpret_cast<uint2 *>(op + k * 32) = make_uint2(Num<T>::pack(a[k].x * inv, a[k].y * inv), Num<T>::pack(a[k].z * inv, a[k].w * inv));
+      }
+      if (p.lse && d0 == 0)
+        p.lse[((long long)b * p.T + t) * p.nq + kv * p.G + g] = L == 0.f ? -INFINITY : (M + log2f(L)) * 0.6931471805599453f;
     }
-    const float inv = L == 0.f ? 0.f : 1.f / L;  // (a NaN stays)
-    if (lane < D / 4)
-      *reinterpret_cast<uint2 *>(p.out + b * p.o_bs + t * p.o_ts + h * p.o_hs + d4 * 8) =
-          make_uint2(Num<T>::pack(a.x * inv, a.y * inv), Num<T>::pack(a.z * inv, a.w * inv));
-    if (p.lse && lane == 0) p.lse[x] = L == 0.f ? -INFINITY : (M + log2f(L)) * 0.6931471805599453f;
+    __syncthreads();
   }
 }
 
@@ -1167,18 +1232,17 @@ template <class T, int D>
 int launch(const AttnDev &p, int sms, cudaStream_t st) {
   const size_t smem = smem_tiles<D>() + sizeof(int) * (p.B + 1);
   const int N = sms * kBlocksPerSm;
-  static_assert(kStages * 2 * kKeys >= kWarps * kRows * 2, "the warps' partials fit into the tiles");
-  int rc = MK_OK;
-  if (p.tc_rows) {
+  static_assert(smem_tiles<D>() >= kWarps * kRows * (D + 4) * 4, "the warps' partials fit into the tiles");
+  // the prefix last: its partials are the larger ones, and the join then finds them in L2
+  int rc = serve_code(cudaFuncSetAttribute((const void *)part_kernel<T, D>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem));
+  if (!rc) rc = serve_launch(part_kernel<T, D>, dim3(N), kWarps * 32, smem, st, false, 1, p);
+  if (!rc && p.tc_rows) {
     rc = serve_code(cudaFuncSetAttribute((const void *)tc_kernel<T, D>, cudaFuncAttributeMaxDynamicSharedMemorySize, tc_smem<D>()));
-    if (!rc) rc = serve_launch(tc_kernel<T, D>, dim3(sms), kTcThreads, tc_smem<D>(), st, false, 1, p);
+    if (!rc) rc = serve_launch(tc_kernel<T, D>, dim3(sms), kTcThreads, tc_smem<D>(), st, true, 1, p);
   }
-  if (!rc)
-    rc = serve_code(cudaFuncSetAttribute((const void *)part_kernel<T, D>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem));
-  if (!rc) rc = serve_launch(part_kernel<T, D>, dim3(N), kWarps * 32, smem, st, p.tc_rows > 0, 1, p);
   if (rc) return rc;
-  const int rows = p.B * p.T * p.nq, grid = std::min((rows + 3) / 4, sms * 16);
-  return serve_launch(join_kernel<T, D>, dim3(grid), 128, sizeof(int) * (p.B + 1), st, true, 1, p, N, sms);
+  const int grid = std::min((p.B * p.T * p.G + kJoinRows - 1) / kJoinRows * p.nkv, sms * 4);
+  return serve_launch(join_kernel<T, D>, dim3(grid), kJoinThreads, sizeof(int) * (p.B + 1), st, true, 1, p, N, sms);
 }
 
 }  // namespace
@@ -1242,7 +1306,7 @@ extern "C" int mk_attn_shared(const mk_attn_shared_args *a, void *workspace, voi
   if ((rc = sm_count(&sms))) return rc;
   const Sizes z = sizes_of(d, a->head_dim, sms);
   char *w = (char *)workspace;
-  d.part_o = (float *)w;
+  d.part_o = (float4 *)w;
   d.tc_o = (float4 *)(w + z.part_o);
   d.part_ml = (float2 *)(w + z.part_o + z.tc_o);
   d.tc_ml = (float2 *)(w + z.part_o + z.tc_o + z.part_ml);

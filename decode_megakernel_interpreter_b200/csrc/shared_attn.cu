@@ -23,11 +23,15 @@ namespace mk {
 namespace {
 
 constexpr int kRows = 16;    // query rows of an item (one m16 matrix instruction)
-constexpr int kKeys = 64;    // positions of a tile
-constexpr int kWarps = 4;    // each takes kKeys / kWarps positions of a tile
-constexpr int kStages = 3;   // tiles in shared memory
-constexpr int kBlocksPerSm = 2;  // of the partial kernel, as many as fit at once
+constexpr int kUnit = 16;    // positions that a warp takes at a time
+constexpr int kWarps = 4;    // of a block of the partial kernel, each on its own
+constexpr int kStages = 2;   // units of a warp in shared memory
+constexpr int kBlocksPerSm = 3;  // of the partial kernel
 constexpr int kMaxRowsB = 1024;
+// A row's maximum only moves when it grows by more than 2^8: until then the
+// weights are at most 2^8, which neither type nor the 32-bit sums mind, and the
+// sums so far need not be rescaled.
+constexpr float kGrow = 8.f;
 
 struct AttnDev {
   const char *q, *k, *v;
@@ -37,12 +41,20 @@ struct AttnDev {
   int32_t *status;
   long long q_bs, q_ts, q_hs, o_bs, o_ts, o_hs, kv_ps, kv_hs, kv_rs;  // bytes
   int B, T, nq, nkv, G, page, n_pages, n_prefix_pages, table_width;
-  int page_shift;  // log2(page), or -1
-  float scale2;  // |scale| * log2(e): scores in powers of two
-  uint32_t flip; // sign bits of two elements of q: set for a negative scale
+  int page_shift;   // log2(page), or -1
+  int page_units;   // a page is a multiple of kUnit: a unit lies in one page of a list
+  float scale2;     // |scale| * log2(e): scores in powers of two
+  uint32_t flip;    // sign bits of two elements of q: set for a negative scale
+  int prefix_tiles;  // row tiles of a K/V head
   int n_prefix_items, own_tiles, n_items;  // items: prefix [kv head][row tile], then own [b][kv head][row tile]
   float4 *part_o;   // [slot][d / 4][kRows]
   float2 *part_ml;  // [slot][kRows]
+  // for the join: how[B] (-1: unused; bit 0: shares the prefix, bit 1: has an
+  // own part), then the first and last worker of each item, of this kernel and
+  // of the tensor cores' (for items that have work)
+  int *how;
+  int2 *who, *tc_who;
+  float inv_G, inv_T;
   // the prefix on the tensor cores (tc_rows > 0; n_prefix_items is 0 then):
   // items [kv head][group of tc_rows rows]
   int tc_rows, tc_groups;
@@ -50,26 +62,19 @@ struct AttnDev {
   float2 *tc_ml;   // [slot][half][kTcRows]
 };
 
-// floor(x / d) for 0 <= x < 2^52, 0 < d, with inv = 1 / d: a 64-bit division
-// costs about a hundred instructions in every thread's way.
-__device__ __forceinline__ long long quotient(long long x, long long d, double inv) {
-  long long q = (long long)((double)x * inv);
-  if (q * d > x) --q;
-  if ((q + 1) * d <= x) ++q;
-  return q;
-}
-
-// The work as a line of K/V tiles: item i owns tiles [start(i), start(i + 1));
-// block c of N takes the c-th equal share of the line, so every block reads
-// the same number of tiles whatever the lengths are.  A block's part of an
-// item is one partial result, in slot c + i: walking along the line, each
-// new part has a larger block or a larger item.
-struct Line {
-  int prefix, prefix_tiles;  // positions and tiles of the prefix
-  long long own0, total;     // where the own items begin, and the end
-  long long N;               // blocks that share it, every one with a tile at least
-  // where the part of block c begins, c <= N
-  __device__ __forceinline__ long long begin(long long c) const { return quotient(c * total, N, 1.0 / (double)N); }
+// `total` pieces of work shared by N workers, N <= total: worker c has
+// [begin(c), begin(c + 1)), equal shares but for one piece.  The items that the
+// pieces belong to follow one another along this line, so every worker does the
+// same amount whatever the lengths are.  A worker's part of an item is one
+// partial result, in slot c + item: walking along the line, each new part has a
+// larger worker or a larger item.
+struct Share {
+  int total, N, each, rest;
+  __device__ __forceinline__ Share(int total_, int workers) : total(total_), N(max(1, min(workers, total_))) {
+    each = total / N;
+    rest = total % N;
+  }
+  __device__ __forceinline__ int begin(int c) const { return c * each + c * rest / N; }
 };
 
 // positions of sequence b (negative: unused), cut to its pages
@@ -78,31 +83,37 @@ __device__ __forceinline__ int seq_len(const AttnDev &p, int b) {
   if (n > cap) report(p.status, MK_ERR_DEVICE_INPUT);
   return min(n, cap);
 }
-// whether every query of sequence b sees the whole prefix
-__device__ __forceinline__ bool shares(const AttnDev &p, int b, int prefix) {
-  return prefix > 0 && seq_len(p, b) - (p.T - 1) >= prefix;
-}
-// the own part of sequence b begins here, and has this many positions
-__device__ __forceinline__ int own_start(const AttnDev &p, int b, int prefix) { return shares(p, b, prefix) ? prefix : 0; }
-__device__ __forceinline__ int own_len(const AttnDev &p, int b, int prefix) {
-  return max(0, seq_len(p, b) - own_start(p, b, prefix));
-}
 __device__ __forceinline__ int prefix_of(const AttnDev &p) {
   const long long cap = (long long)p.n_prefix_pages * p.page, n = p.n_prefix_pages > 0 ? p.prefix_len[0] : 0;
   if ((n < 0 || n > cap) && threadIdx.x == 0) report(p.status, MK_ERR_DEVICE_INPUT);
   return (int)max(0ll, min(n, cap));
 }
+// How sequence b of length n goes: it shares the prefix if every query sees all
+// of it; its own part begins behind it, or at 0.
+__device__ __forceinline__ bool shares(const AttnDev &p, int n, int prefix) { return prefix > 0 && n - (p.T - 1) >= prefix; }
+// Units of the positions [lo, hi): multiples of kUnit, the first and last may
+// lie partly outside.
+__device__ __forceinline__ int units(int lo, int hi) { return hi > lo ? (hi + kUnit - 1) / kUnit - lo / kUnit : 0; }
 
-// Tiles of one own item of each sequence as prefix sums: sum[b] = tiles of the
-// sequences before b (sum: B + 1 ints).  Called by the whole block.
-__device__ Line make_line(const AttnDev &p, int blocks, int *sum, int *red) {
-  Line l;
-  l.prefix = prefix_of(p);
-  l.prefix_tiles = (l.prefix + kKeys - 1) / kKeys;
+// The line of the partial kernel's items, in units: prefix items, then own
+// items; sum[b] = units of one own item of each sequence before b.
+struct Line {
+  int prefix, prefix_units, own0;  // own0: where the own items begin
+  Share share;
+  __device__ __forceinline__ Line(const AttnDev &p, int prefix_, int own_units, int workers)
+      : prefix(prefix_), prefix_units(units(0, prefix_)), own0(p.n_prefix_items * prefix_units),
+        share(own0 + own_units * p.nkv * p.own_tiles, workers) {}
+};
+// sum (B + 1 ints of shared memory) and the prefix's length; called by the whole block.
+__device__ int make_sums(const AttnDev &p, int *sum, int *red) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, per = (p.B + blockDim.x - 1) / blockDim.x;
-  const int b0 = min((int)threadIdx.x * per, p.B), b1 = min(b0 + per, p.B);
+  const int b0 = min((int)threadIdx.x * per, p.B), b1 = min(b0 + per, p.B), prefix = prefix_of(p);
+  auto own = [&](int b) {
+    const int n = seq_len(p, b);
+    return units(shares(p, n, prefix) ? prefix : 0, n);
+  };
   int mine = 0;
-  for (int b = b0; b < b1; ++b) mine += (own_len(p, b, l.prefix) + kKeys - 1) / kKeys;
+  for (int b = b0; b < b1; ++b) mine += own(b);
   int x = warp_incl_sum(mine);
   if (lane == 31) red[warp] = x;
   __syncthreads();
@@ -110,19 +121,24 @@ __device__ Line make_line(const AttnDev &p, int blocks, int *sum, int *red) {
   x -= mine;
   for (int b = b0; b < b1; ++b) {
     sum[b] = x;
-    x += (own_len(p, b, l.prefix) + kKeys - 1) / kKeys;
+    x += own(b);
   }
   if (b0 < b1 && b1 == p.B) sum[p.B] = x;
   __syncthreads();
-  l.own0 = (long long)p.n_prefix_items * l.prefix_tiles;
-  l.total = l.own0 + (long long)sum[p.B] * p.nkv * p.own_tiles;
-  l.N = min((long long)blocks, l.total);
-  return l;
+  if (blockIdx.x == 0)  // for the join
+    for (int b = threadIdx.x; b < p.B; b += blockDim.x) {
+      const int n = seq_len(p, b);
+      p.how[b] = n < 0 ? -1 : (shares(p, n, prefix) ? 1 : 0) | (sum[b + 1] > sum[b] ? 2 : 0);
+    }
+  return prefix;
 }
 
 __device__ __forceinline__ uint32_t smem_addr(const void *p) { return (uint32_t)__cvta_generic_to_shared(p); }
 __device__ __forceinline__ void cp16(uint32_t dst, const void *src, bool live) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(live ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void cp16(uint32_t dst, const void *src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
 }
 __device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N>
@@ -172,7 +188,7 @@ struct Num;
 template <>
 struct Num<__nv_bfloat16> {
   static __device__ __forceinline__ void mma(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
                  : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
                  : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
   }
@@ -190,7 +206,7 @@ struct Num<__nv_bfloat16> {
 template <>
 struct Num<__half> {
   static __device__ __forceinline__ void mma(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
                  : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
                  : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
   }
@@ -206,20 +222,20 @@ struct Num<__half> {
   }
 };
 
-// Shared memory of the partial kernel: each warp's stages (its rows of K, then
-// of V), reused at an item's end for the warps' partials; then the line's sums.
+// Shared memory of the partial kernel: each warp's stages (a unit's rows of K,
+// then of V); then the line's sums.
 template <int D>
-constexpr int tile_bytes() {
-  return kKeys * D * 2;
+constexpr int smem_stage() {
+  return 2 * kUnit * D * 2;
 }
 template <int D>
-constexpr int smem_tiles() {
-  return kStages * 2 * tile_bytes<D>();
+constexpr int smem_stages() {
+  return kWarps * kStages * smem_stage<D>();
 }
 
-// Where 16-byte chunk c of row r of a tile stands: rows of D elements, the
+// Where 16-byte chunk c of row r of a unit stands: rows of D elements, the
 // chunks of each group of eight exchanged by the row number so that eight rows'
-// same chunk lies in eight different banks groups.
+// same chunk lies in eight different groups of banks.
 template <int D>
 __device__ __forceinline__ uint32_t at(int r, int c) {
   return (uint32_t)(r * (D * 2) + ((c ^ (r & 7)) << 4));
@@ -237,46 +253,78 @@ __device__ __forceinline__ long long row_offset(const AttnDev &p, int pos, int p
   }
   return pg * p.kv_ps + (pos - page_index(p, pos) * p.page) * p.kv_rs;
 }
+// Copy 16 rows, the positions pos .. pos + 15, to shared memory: K and, `gap`
+// bytes on, V (kBoth), or one of the two.  pg: the page of all of them (`one`),
+// or of position pos + lane % 16; rows outside [lo, hi) become zeros.  to: where
+// the lane's chunk of the lane's first row goes, an offset from `base` whose
+// bits 4-6 are exchanged with the row number's; rows are kRow bytes apart.
+template <int D, bool kBoth, int kRow>
+__device__ __forceinline__ void copy_rows(const AttnDev &p, const char *k, const char *v, int kv, int pos, int lo, int hi,
+                                          bool one, int pg, uint32_t base, uint32_t to, uint32_t gap) {
+  const int lane = threadIdx.x & 31;
+  constexpr int kChunks = D / 8, kPass = 32 / kChunks;  // rows of one instruction
+  const int ch = lane % kChunks, r0 = lane / kChunks;
+  const long long off = row_offset(p, pos + (one ? 0 : lane & 15), pg), head = kv * p.kv_hs + ch * 16;
+  if (one && pos >= lo && pos + 16 <= hi) {
+    const long long step = kPass * p.kv_rs, o = head + off + r0 * p.kv_rs;
+    const char *ks = k + o, *vs = v + o;
+#pragma unroll
+    for (int x = 0; x < 16 / kPass; ++x, ks += step, vs += step) {
+      const uint32_t dst = base + (to ^ (x * kPass & 7) << 4) + x * kPass * kRow;
+      cp16(dst, ks);
+      if (kBoth) cp16(dst + gap, vs);
+    }
+    return;
+  }
+#pragma unroll
+  for (int x = 0; x < 16 / kPass; ++x) {
+    const int r = x * kPass + r0;
+    const long long o = head + (one ? off + r * p.kv_rs : __shfl_sync(0xffffffffu, off, r));
+    const bool live = pos + r >= lo && pos + r < hi;
+    const uint32_t dst = base + (to ^ (x * kPass & 7) << 4) + x * kPass * kRow;
+    cp16(dst, k + (live ? o : 0), live);
+    if (kBoth) cp16(dst + gap, v + (live ? o : 0), live);
+  }
+}
 
-// The warps of a block work on their own: warp w copies, and attends over, the
-// positions 16 w .. 16 w + 15 of every tile, kStages tiles deep, without a
-// barrier until an item's end.  A lane looks up the page of one position, a
-// tile ahead of the copies that need it.
+// A warp takes a share of the line on its own: 16 rows of Q in registers, units
+// of 16 positions through two stages of shared memory, no barrier.  Such items
+// are small (a sequence's own part, or a prefix with few rows), so what counts
+// is how many of them wait for memory at once: 12 warps an SM, each with the
+// next unit in flight.
 template <class T, int D>
 __global__ void __launch_bounds__(kWarps * 32, kBlocksPerSm) part_kernel(const AttnDev p) {
   extern __shared__ __align__(128) char sm[];
   __shared__ int red[kWarps];
-  __shared__ float m_s[kWarps][kRows], l_s[kWarps][kRows];
-  int *sum = reinterpret_cast<int *>(sm + smem_tiles<D>());
+  int *sum = reinterpret_cast<int *>(sm + smem_stages<D>());
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  constexpr int kHalf = kRows * D * 2, kStage = 2 * kHalf;  // bytes of a warp's 16 rows of K; of K and V
+  constexpr int kHalf = kUnit * D * 2, kStage = 2 * kHalf;
   char *const mine = sm + warp * kStages * kStage;
   const uint32_t mine_a = smem_addr(mine);
   pdl_wait();
   pdl_trigger();
-  const Line line = make_line(p, gridDim.x, sum, red);
-  const long long c = blockIdx.x;
-  long long t0 = c < line.N ? line.begin(c) : 0;
-  const long long t_end = c < line.N ? line.begin(c + 1) : 0;
+  const int prefix = make_sums(p, sum, red);
+  const Line line(p, prefix, sum[p.B], gridDim.x * kWarps);
+  const int c = warp * gridDim.x + blockIdx.x;  // (neighbours along the line on different SMs)
+  int t0 = c < line.share.N && line.share.total > 0 ? line.share.begin(c) : 0;
+  const int t_end = c < line.share.N && line.share.total > 0 ? line.share.begin(c + 1) : 0;
 
   while (t0 < t_end) {
-    // ---- which item, and which of its tiles
+    // ---- which item, and which of its units
     int item, kv, row0, n_rows, lo, hi;  // rows row0.. of the item's row list; positions [lo, hi) of the sequence
     int b = -1;                          // own item's sequence
-    long long item_t0, item_t1;
+    int item_t0, item_n;
     if (t0 < line.own0) {
-      item = (int)quotient(t0, line.prefix_tiles, 1.0 / line.prefix_tiles);
-      item_t0 = (long long)item * line.prefix_tiles;
-      item_t1 = item_t0 + line.prefix_tiles;
-      const int tiles = p.n_prefix_items / p.nkv;
-      kv = item / tiles;
-      row0 = item % tiles * kRows;
+      item = t0 / line.prefix_units;
+      item_t0 = item * line.prefix_units;
+      item_n = line.prefix_units;
+      kv = item / p.prefix_tiles;
+      row0 = item % p.prefix_tiles * kRows;
       n_rows = min(kRows, p.B * p.T * p.G - row0);
       lo = 0;
-      hi = line.prefix;
+      hi = prefix;
     } else {
-      const int per = p.nkv * p.own_tiles;
-      const int y = (int)quotient(t0 - line.own0, per, 1.0 / per);  // sum[b] <= y < sum[b + 1]
+      const int per = p.nkv * p.own_tiles, y = (t0 - line.own0) / per;  // sum[b] <= y < sum[b + 1]
       int x0 = 0, x1 = p.B;
       while (x1 - x0 > 1) {
         const int mid = (x0 + x1) / 2;
@@ -284,70 +332,55 @@ __global__ void __launch_bounds__(kWarps * 32, kBlocksPerSm) part_kernel(const A
         else x1 = mid;
       }
       b = x0;
-      const int nt = sum[b + 1] - sum[b];
-      const long long base = line.own0 + (long long)sum[b] * per;
-      const int k = (int)quotient(t0 - base, nt, 1.0 / nt);
+      item_n = sum[b + 1] - sum[b];
+      const int base = line.own0 + sum[b] * per, k = (t0 - base) / item_n;
       item = p.n_prefix_items + b * per + k;
-      item_t0 = base + (long long)k * nt;
-      item_t1 = item_t0 + nt;
+      item_t0 = base + k * item_n;
       kv = k / p.own_tiles;
       row0 = k % p.own_tiles * kRows;
       n_rows = min(kRows, p.T * p.G - row0);
-      lo = own_start(p, b, line.prefix);
-      hi = lo + own_len(p, b, line.prefix);
+      hi = seq_len(p, b);
+      lo = shares(p, hi, prefix) ? prefix : 0;
     }
-    const int first = (int)(t0 - item_t0), n_tiles = (int)(min(t_end, item_t1) - t0);
-    t0 += n_tiles;
+    const int first = t0 - item_t0, n = min(t_end, item_t0 + item_n) - t0;
+    t0 += n;
+    if (lane == 0) {
+      if (first == 0) p.who[item].x = c;
+      if (first + n == item_n) p.who[item].y = c;
+    }
 
     const int *table = p.table + (long long)b * p.table_width;  // (not used by prefix items)
-    const int key0 = lo + first * kKeys + warp * 16;  // this warp's first position
-    auto look_up = [&](int i) {  // the page of this lane's position of tile i (lanes 16-31: as 0-15)
-      const int pos = key0 + i * kKeys + (lane & 15);
-      return i < n_tiles && pos < hi ? (pos < line.prefix ? p.prefix_pages : table)[page_index(p, pos)] : 0;
+    const int key0 = (lo / kUnit + first) * kUnit;              // this part's first position
+    // whether unit i is in one page: not where a sequence that does not share
+    // the prefix leaves the prefix's list for its own in the middle of it
+    auto one_page = [&](int i) {
+      const int pos = key0 + i * kUnit;
+      return p.page_units && !(lo < prefix && pos < prefix && pos + kUnit > prefix);
     };
-    auto load = [&](int i, int pg) {  // tile i into stage i % kStages
-      const long long off = row_offset(p, key0 + i * kKeys + (lane & 15), pg);
-      const uint32_t dst = mine_a + (i % kStages) * kStage;
-      constexpr int kChunks = D / 8, kPass = 32 / kChunks;  // rows of one instruction
-      const int ch = lane % kChunks, r0 = lane / kChunks, left = hi - (key0 + i * kKeys);
-#pragma unroll
-      for (int x = 0; x < 16 / kPass; ++x) {
-        const int r = x * kPass + r0;
-        const long long o = __shfl_sync(0xffffffffu, off, r) + kv * p.kv_hs + ch * 16;
-        const bool live = r < left;
-        cp16(dst + at<D>(r, ch), p.k + o, live);
-        cp16(dst + kHalf + at<D>(r, ch), p.v + o, live);
-      }
+    auto look_up = [&](int i) {  // the page of unit i, or of this lane's position of it
+      const int pos = key0 + i * kUnit + (one_page(i) ? 0 : lane & 15), at = max(pos, lo);
+      return i < n && at < hi ? (at < prefix ? p.prefix_pages : table)[page_index(p, at)] : 0;
     };
-    int pg[kStages];  // pages of the tiles to come
-#pragma unroll
-    for (int i = 0; i < kStages; ++i) pg[i] = look_up(i);
-#pragma unroll
-    for (int i = 0; i < kStages - 1; ++i) {
-      if (i < n_tiles) load(i, pg[i]);
-      cp_commit();
-    }
-    int ahead = pg[kStages - 1];
+    auto load = [&](int i, int pg) {  // unit i into stage i % kStages
+      copy_rows<D, true, D * 2>(p, p.k, p.v, kv, key0 + i * kUnit, lo, hi, one_page(i), pg, mine_a + (i & 1) * kStage,
+                                at<D>(lane / (D / 8), lane % (D / 8)), kHalf);
+    };
+    load(0, look_up(0));
+    cp_commit();
+    int ahead = look_up(1);
 
-    // ---- this thread's rows: r and r + 8 of the tile (g = lane / 4)
-    auto row_of = [&](int r, int &rb, int &rt, int &rh) {
-      const int x = row0 + r;
-      rh = kv * p.G + x % p.G;
-      rt = x / p.G % p.T;
-      rb = b >= 0 ? b : x / p.G / p.T;
-    };
+    // ---- this thread's rows: r and r + 8 of the tile (r = lane / 4)
     uint32_t qf[D / 16][4];
     int sees[2], min_sees = hi;  // positions that the row sees
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-      const int r = lane / 4 + 8 * h;
+      const int r = lane / 4 + 8 * h, x = row0 + r;
       sees[h] = 0;
       const char *qp = nullptr;
       if (r < n_rows) {
-        int rb, rt, rh;
-        row_of(r, rb, rt, rh);
+        const int rh = kv * p.G + x % p.G, rt = x / p.G % p.T, rb = b >= 0 ? b : x / p.G / p.T;
         // (a row that does not see all of the prefix does not take this part)
-        sees[h] = b < 0 ? hi : max(0, max(seq_len(p, rb), 0) - (p.T - 1 - rt));
+        sees[h] = b < 0 ? hi : max(0, hi - (p.T - 1 - rt));
         qp = p.q + rb * p.q_bs + rt * p.q_ts + rh * p.q_hs;
         min_sees = min(min_sees, sees[h]);
       }
@@ -363,16 +396,15 @@ __global__ void __launch_bounds__(kWarps * 32, kBlocksPerSm) part_kernel(const A
 #pragma unroll
     for (int i = 0; i < D / 8; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
 
-    for (int i = 0; i < n_tiles; ++i) {
-      const int next = look_up(i + kStages);
-      cp_wait<kStages - 2>();
+    for (int i = 0; i < n; ++i) {
+      const int next = look_up(i + 2);
+      cp_wait<0>();
       __syncwarp();
-      if (i + kStages - 1 < n_tiles) load(i + kStages - 1, ahead);
+      if (i + 1 < n) load(i + 1, ahead);
       cp_commit();
       ahead = next;
-      const int pos0 = key0 + i * kKeys;
-      if (pos0 >= hi) continue;
-      const char *kt = mine + (i % kStages) * kStage, *vt = kt + kHalf;
+      const int pos0 = key0 + i * kUnit;
+      const char *kt = mine + (i & 1) * kStage, *vt = kt + kHalf;
       const uint32_t ka = smem_addr(kt), va = ka + kHalf;
       // ---- scores: 16 rows x 16 positions
       float s[2][4] = {};
@@ -383,41 +415,52 @@ __global__ void __launch_bounds__(kWarps * 32, kBlocksPerSm) part_kernel(const A
         Num<T>::mma(s[0], qf[k], kf[0], kf[1]);
         Num<T>::mma(s[1], qf[k], kf[2], kf[3]);
       }
-      const bool edge = pos0 + 16 > min(min_sees, hi);
+      const bool edge = pos0 < lo || pos0 + kUnit > min(min_sees, hi);
       if (edge) {
 #pragma unroll
         for (int n = 0; n < 2; ++n)
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
             const int pos = pos0 + n * 8 + (lane & 3) * 2 + (e & 1);
-            if (pos >= min(sees[e >> 1], hi)) s[n][e] = -INFINITY;
+            if (pos < lo || pos >= min(sees[e >> 1], hi)) s[n][e] = -INFINITY;
           }
       }
       // ---- running maximum and sum of each row (32-bit; scores in powers of two)
+      float top[2];
+      bool grow = false;
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
         float x = fmaxf(fmaxf(s[0][2 * h], s[0][2 * h + 1]), fmaxf(s[1][2 * h], s[1][2 * h + 1]));
         x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 1));
         x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 2));
-        // (a row that has seen nothing yet: x = -inf, whatever the scale)
-        const float mn = fmaxf(m[h], x == -INFINITY ? x : x * p.scale2), base = mn == -INFINITY ? 0.f : mn;
-        const float f = exp2_(m[h] - base);
-        m[h] = mn;
+        top[h] = x * p.scale2;
+        grow |= top[h] > (m[h] == -INFINITY ? m[h] : m[h] + kGrow);
+      }
+      if (__any_sync(0xffffffffu, grow)) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const float f = top[h] > m[h] ? exp2_(m[h] - top[h]) : 1.f;
+          m[h] = fmaxf(m[h], top[h]);
+          l[h] *= f;
+#pragma unroll
+          for (int d = 0; d < D / 8; ++d) {
+            o[d][2 * h] *= f;
+            o[d][2 * h + 1] *= f;
+          }
+        }
+      }
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const float base = m[h] == -INFINITY ? 0.f : m[h];
         float t = 0.f;
 #pragma unroll
         for (int n = 0; n < 2; ++n)
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
-            const float y = s[n][2 * h + e];
-            s[n][2 * h + e] = y == -INFINITY ? 0.f : exp2_(fmaf(y, p.scale2, -base));
+            s[n][2 * h + e] = exp2_(fmaf(s[n][2 * h + e], p.scale2, -base));
             t += s[n][2 * h + e];
           }
-        l[h] = l[h] * f + t;
-#pragma unroll
-        for (int d = 0; d < D / 8; ++d) {
-          o[d][2 * h] *= f;
-          o[d][2 * h + 1] *= f;
-        }
+        l[h] += t;
       }
       if (edge) {
         // A masked position's V may hold an infinity or a NaN, which p = 0
@@ -436,7 +479,7 @@ __global__ void __launch_bounds__(kWarps * 32, kBlocksPerSm) part_kernel(const A
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
               const float w = __shfl_sync(0xffffffffu, s[j / 8][2 * h + (j & 1)], (lane & ~3) | ((j & 7) >> 1));
-              if (pos0 + j >= min(sees[h], hi)) continue;
+              if (pos0 + j < lo || pos0 + j >= min(sees[h], hi)) continue;
 #pragma unroll
               for (int d = 0; d < D / 8; ++d) {
                 const float2 v = Num<T>::unpack(
@@ -464,56 +507,27 @@ __global__ void __launch_bounds__(kWarps * 32, kBlocksPerSm) part_kernel(const A
         uint32_t vf[4];  // positions 0-7 and 8-15 of columns 0-7, then of columns 8-15
         ldsm4t(vf, va + at<D>(lane & 15, d * 2 + (lane >> 4)));
         Num<T>::mma(o[2 * d], ph, vf[0], vf[1]);
-        Num<T>::mma(o[2 * d], pl, vf[0], vf[1]);
         Num<T>::mma(o[2 * d + 1], ph, vf[2], vf[3]);
+        Num<T>::mma(o[2 * d], pl, vf[0], vf[1]);
         Num<T>::mma(o[2 * d + 1], pl, vf[2], vf[3]);
       }
     }
-    cp_wait<0>();
-    __syncthreads();  // the stages become the warps' partials
+    __syncwarp();  // the stages are read
 
-    // ---- join the warps and store the block's partial of this item
+    // ---- the warp's partial of this item
+    const int slot = c + item;
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
+      const int r = lane / 4 + 8 * h;
       l[h] += __shfl_xor_sync(0xffffffffu, l[h], 1);
       l[h] += __shfl_xor_sync(0xffffffffu, l[h], 2);
-      if ((lane & 3) == 0) {
-        m_s[warp][lane / 4 + 8 * h] = m[h];
-        l_s[warp][lane / 4 + 8 * h] = l[h];
-      }
-    }
-    float *po = reinterpret_cast<float *>(sm);  // [warp][row][D + 4]
-#pragma unroll
-    for (int d = 0; d < D / 8; ++d)
-#pragma unroll
-      for (int h = 0; h < 2; ++h)
-        *reinterpret_cast<float2 *>(po + (warp * kRows + lane / 4 + 8 * h) * (D + 4) + d * 8 + (lane & 3) * 2) =
-            make_float2(o[d][2 * h], o[d][2 * h + 1]);
-    __syncthreads();
-    const long long slot = c + item;
-    for (int x = tid; x < kRows * (D / 4); x += kWarps * 32) {
-      const int r = x % kRows, d = x / kRows;
       if (r >= n_rows) continue;
-      float M = -INFINITY;
+      if ((lane & 3) == 0) p.part_ml[(long long)slot * kRows + r] = make_float2(m[h], l[h]);
+      float2 *to = reinterpret_cast<float2 *>(p.part_o + (long long)slot * (D / 4) * kRows + r) + (lane & 1);
 #pragma unroll
-      for (int w = 0; w < kWarps; ++w) M = fmaxf(M, m_s[w][r]);
-      const float base = M == -INFINITY ? 0.f : M;
-      float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
-      float L = 0.f;
-#pragma unroll
-      for (int w = 0; w < kWarps; ++w) {
-        const float f = exp2_(m_s[w][r] - base);
-        const float4 y = *reinterpret_cast<const float4 *>(po + (w * kRows + r) * (D + 4) + d * 4);
-        a.x += f * y.x;
-        a.y += f * y.y;
-        a.z += f * y.z;
-        a.w += f * y.w;
-        L += f * l_s[w][r];
-      }
-      p.part_o[(slot * (D / 4) + d) * kRows + r] = a;
-      if (d == 0) p.part_ml[slot * kRows + r] = make_float2(M, L);
+      for (int d = 0; d < D / 8; ++d)
+        to[(d * 2 + (lane >> 1 & 1)) * kRows * 2] = make_float2(o[d][2 * h], o[d][2 * h + 1]);
     }
-    __syncthreads();  // before the next item's tiles
   }
 }
 
@@ -525,20 +539,18 @@ __global__ void __launch_bounds__(kWarps * 32, kBlocksPerSm) part_kernel(const A
 //   tc_rows = 256: the halves take 128 rows each and read the same K/V tiles;
 //   tc_rows = 128: both take the same rows, and every other K/V tile.
 // Each half has two S of 64 positions: the tensor cores fill one while the
-// softmax works on the other.  Four warps copy the K/V tiles (16 bytes a time,
+// softmax works on the other.  Two warps copy the K/V tiles (16 bytes a time,
 // rows from the page list) into a ring in the order they are needed, and a
 // warp for each half issues its matrix instructions (one warp for both spent
 // longer on the waits and descriptors than the instructions took).
 // P takes S's place in tensor memory, rounded to the operands' type: half a
 // step (2^-8 or 2^-11) of each weight, as the output's own rounding.
-// A row's maximum only moves when it grows by more than 2^8: until then the
-// weights are at most 2^8, which neither type nor the 32-bit sums mind, and O
-// need not be rescaled.
 
 constexpr int kTcRows = 128;  // rows of a half
 constexpr int kTcKeys = 64;   // positions of a tile
-constexpr int kTcThreads = 14 * 32;  // warps 0-3 and 4-7: softmax; 8-11: copies; 12 and 13: matrix instructions
-constexpr float kTcGrow = 8.f;
+// warps 0-3 and 4-7: softmax; 8 and 9: copies; 10 and 11: matrix instructions.
+// (With a thirteenth warp a thread could have 128 registers only.)
+constexpr int kTcThreads = 12 * 32;
 template <int D>
 constexpr int tc_tile() {
   return kTcKeys * D * 2;
@@ -689,35 +701,16 @@ struct TcOrder {
   int n, ahead;
   __device__ __forceinline__ int k_at(int j) const { return j < ahead ? j : 2 * j - ahead + 1; }
   __device__ __forceinline__ int v_at(int j) const { return j < n - ahead ? ahead + 2 * j : n + j; }
-  __device__ __forceinline__ int tile(int e, bool &is_v) const {  // of entry e
-    is_v = e >= ahead && (e >= 2 * n - ahead || !((e - ahead) & 1));
-    return !is_v ? (e < ahead ? e : (e + ahead - 1) / 2) : e < 2 * n - ahead ? (e - ahead) / 2 : e - n;
-  }
+  __device__ __forceinline__ bool is_v(int e) const { return e >= ahead && (e >= 2 * n - ahead || !((e - ahead) & 1)); }
 };
 
-// The blocks' line of tiles, as for the other items.
+// The blocks' line of tiles.
 struct TcLine {
-  int prefix, tiles, n_items;
-  long long total, N;
-  double inv_tiles;
-  __device__ __forceinline__ long long begin(long long c) const { return quotient(c * total, N, 1.0 / (double)N); }
-  // the item that tile t is of, and which of its tiles it is
-  __device__ __forceinline__ int item_of(long long t, int &first) const {
-    const int i = (int)quotient(t, tiles, inv_tiles);
-    first = (int)(t - (long long)i * tiles);
-    return i;
-  }
+  int tiles;
+  Share share;
+  __device__ __forceinline__ TcLine(const AttnDev &p, int prefix, int blocks)
+      : tiles((prefix + kTcKeys - 1) / kTcKeys), share(tiles * p.nkv * p.tc_groups, blocks) {}
 };
-__device__ __forceinline__ TcLine tc_line(const AttnDev &p, int prefix, int blocks) {
-  TcLine l;
-  l.prefix = prefix;
-  l.tiles = (prefix + kTcKeys - 1) / kTcKeys;
-  l.n_items = p.nkv * p.tc_groups;
-  l.total = (long long)l.tiles * l.n_items;
-  l.N = min((long long)blocks, l.total);
-  l.inv_tiles = l.tiles > 0 ? 1.0 / l.tiles : 0.0;
-  return l;
-}
 
 template <class T, int D>
 __global__ void __launch_bounds__(kTcThreads, 1) tc_kernel(const AttnDev p) {
@@ -731,7 +724,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) tc_kernel(const AttnDev p) {
   const bool pair = p.tc_rows == 2 * kTcRows;  // the halves have rows of their own
   if (tid == 0) {
     for (int i = 0; i < kRing; ++i) {
-      bar_init(&sh.full[i], 128);
+      bar_init(&sh.full[i], 64);
       bar_init(&sh.empty[i], pair ? 2 : 1);
     }
     for (int w = 0; w < 2; ++w) {
@@ -747,7 +740,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) tc_kernel(const AttnDev p) {
     sh.dead = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
-  if (warp == 12)
+  if (warp == 10)
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_addr(&sh.tmem)) : "memory");
   // This kernel starts as blocks of the own parts' kernel end.  It reads
   // nothing of theirs, and only waits for them before it ends itself.
@@ -756,59 +749,56 @@ __global__ void __launch_bounds__(kTcThreads, 1) tc_kernel(const AttnDev p) {
   __syncthreads();
   tc_after();
   const uint32_t tm = sh.tmem;
-  const TcLine line = tc_line(p, prefix_of(p), gridDim.x);
-  const long long c = blockIdx.x;
+  const int prefix = prefix_of(p), c = blockIdx.x;
+  const TcLine line(p, prefix, gridDim.x);
   const int dist = pair ? 2 : 4;               // K tiles that are multiplied ahead of their V
   const int R = p.B * p.T * p.G;
-  const long long t_begin = c < line.N ? line.begin(c) : 0, t_end = c < line.N ? line.begin(c + 1) : 0;
+  const bool any = c < line.share.N && line.tiles > 0;
+  const int t_begin = any ? line.share.begin(c) : 0, t_end = any ? line.share.begin(c + 1) : 0;
   auto s_of = [&](int w, int i) { return tm + w * 128 + i * 64; };
   auto o_of = [&](int w) { return tm + 256 + w * D; };
 
-  if (warp >= 8 && warp < 12) {
-    // ---------------- copies: warp w of the four takes rows 16 w .. 16 w + 15
-    // of every tile; a lane looks up the page of one, three entries ahead
+  if (warp >= 8 && warp < 10) {
+    // ---------------- copies: warp w of the two takes rows 32 w .. 32 w + 31
+    // of every tile, 16 at a time
     int g = 0;  // ring entries begun
     bool ok = true;
-    const int row = (warp - 8) * 16;
-    for (long long t0 = t_begin; ok && t0 < t_end;) {
-      int first;
-      const int item = line.item_of(t0, first);
-      const int n = (int)min(t_end - t0, (long long)(line.tiles - first)), kv = item / p.tc_groups;
+    const int row = (warp - 8) * 32, ch = lane % (D / 8), r0 = lane / (D / 8);
+    for (int t0 = t_begin; ok && t0 < t_end;) {
+      const int item = t0 / line.tiles, first = t0 % line.tiles, n = min(t_end - t0, line.tiles - first), kv = item / p.tc_groups;
       t0 += n;
-      const TcOrder order{n, min(dist, n)};
-      auto look_up = [&](int e) {
-        bool v;
-        const int pos = (first + order.tile(e, v)) * kTcKeys + row + (lane & 15);
-        return e < 2 * n && pos < line.prefix ? p.prefix_pages[page_index(p, pos)] : 0;
+      // Pages: where 16 rows are in one page, lane i looks up those of tile j + i
+      // for the next 32 tiles; else a lane looks up that of one row, each time.
+      auto look_up = [&](int j) {
+        const int pos = p.page_units ? (first + j + lane) * kTcKeys + row : (first + j) * kTcKeys + row + (lane & 15);
+        return make_int2(pos < prefix ? p.prefix_pages[page_index(p, pos)] : 0,
+                         pos + 16 < prefix ? p.prefix_pages[page_index(p, pos + 16)] : 0);
       };
-      int pg0 = look_up(0), pg1 = look_up(1), pg2 = look_up(2);
+      const TcOrder order{n, min(dist, n)};
+      int j_of[2] = {0, 0};  // the next K, the next V
+      int2 pages[2] = {};
       for (int e = 0; e < 2 * n; ++e) {
-        const int pg = pg0;
-        pg0 = pg1;
-        pg1 = pg2;
-        pg2 = look_up(e + 3);
-        bool is_v;
-        const int slot = g % kRing, j = order.tile(e, is_v);
+        const bool is_v = order.is_v(e);
+        const int slot = g % kRing, j = is_v ? j_of[1]++ : j_of[0]++;
+        int2 pg = is_v ? pages[1] : pages[0];
+        if (!p.page_units || j % 32 == 0) pg = look_up(j);
+        if (is_v) pages[1] = pg;
+        else pages[0] = pg;
+        if (p.page_units) pg = make_int2(__shfl_sync(0xffffffffu, pg.x, j % 32), __shfl_sync(0xffffffffu, pg.y, j % 32));
         if (g >= kRing) ok = bar_wait_all(&sh, &sh.empty[slot], ((g / kRing) & 1) ^ 1, p.status);
         if (!ok) break;
         const uint32_t dst = ring + slot * tc_tile<D>();
-        constexpr int kChunks = D / 8, kPass = 32 / kChunks;
-        const int ch = lane % kChunks, r0 = lane / kChunks, left = line.prefix - (first + j) * kTcKeys - row;
-        const char *from = (is_v ? p.v : p.k) + kv * p.kv_hs + ch * 16;
-        const long long off = row_offset(p, (first + j) * kTcKeys + row + (lane & 15), pg);
-#pragma unroll
-        for (int x = 0; x < 16 / kPass; ++x) {
-          const int r = x * kPass + r0;
-          const long long o = __shfl_sync(0xffffffffu, off, r);
-          cp16(dst + tc_at(kTcKeys, row + r, ch), from + o, r < left);
-        }
+        const char *src = is_v ? p.v : p.k;
+        const int pos = (first + j) * kTcKeys + row;
+        copy_rows<D, false, 128>(p, src, src, kv, pos, 0, prefix, p.page_units, pg.x, dst, tc_at(kTcKeys, row + r0, ch), 0);
+        copy_rows<D, false, 128>(p, src, src, kv, pos + 16, 0, prefix, p.page_units, pg.y, dst, tc_at(kTcKeys, row + 16 + r0, ch), 0);
         cp_arrive(&sh.full[slot]);
         ++g;
       }
     }
     cp_commit();
     cp_wait<0>();
-  } else if (warp >= 12) {
+  } else if (warp >= 10) {
     // ---------------- matrix instructions of half w: the warp walks as one, an
     // elected lane issues
     constexpr uint32_t kType = std::is_same<T, __nv_bfloat16>::value ? 1u : 0u;
@@ -816,7 +806,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) tc_kernel(const AttnDev p) {
     // leading dimension the other way round
     constexpr uint32_t kS = (1u << 4) | (kType << 7) | (kType << 10) | ((kTcKeys / 8u) << 17) | ((128u / 16) << 24);
     constexpr uint32_t kO = (1u << 4) | (kType << 7) | (kType << 10) | (1u << 16) | ((uint32_t)(D / 8) << 17) | ((128u / 16) << 24);
-    const int w = warp - 12;
+    const int w = warp - 10;
     const uint32_t q_low = tc_low(base, 16) + w * (kTcRows * D * 2 >> 4);
     const uint32_t k_low = tc_low(ring, 16), v_low = tc_low(ring, kTcKeys * 128);
     int g = 0;                          // ring entries before this item
@@ -840,11 +830,13 @@ __global__ void __launch_bounds__(kTcThreads, 1) tc_kernel(const AttnDev p) {
       }
       __syncwarp();
     };
-    for (long long t0 = t_begin; ok && t0 < t_end;) {
-      int first;
-      const int item = line.item_of(t0, first);
-      const int n = (int)min(t_end - t0, (long long)(line.tiles - first));
+    for (int t0 = t_begin; ok && t0 < t_end;) {
+      const int item = t0 / line.tiles, first = t0 % line.tiles, n = min(t_end - t0, line.tiles - first);
       t0 += n;
+      if (w == 0 && lane == 0) {
+        if (first == 0) p.tc_who[item].x = c;
+        if (first + n == line.tiles) p.tc_who[item].y = c;
+      }
       const TcOrder order{n, min(dist, n)};
       // this half's tiles: all (pair) or every other; its k-th S is in buffer k & 1
       const int step = pair ? 1 : 2, j0 = pair ? 0 : w;
@@ -899,10 +891,8 @@ __global__ void __launch_bounds__(kTcThreads, 1) tc_kernel(const AttnDev p) {
     uint32_t s_phase = 0;  // bit i
     int done = 0;          // tiles of this half so far
     bool ok = true;
-    for (long long t0 = t_begin; ok && t0 < t_end;) {
-      int first;
-      const int item = line.item_of(t0, first);
-      const int n = (int)min(t_end - t0, (long long)(line.tiles - first)), kv = item / p.tc_groups;
+    for (int t0 = t_begin; ok && t0 < t_end;) {
+      const int item = t0 / line.tiles, first = t0 % line.tiles, n = min(t_end - t0, line.tiles - first), kv = item / p.tc_groups;
       t0 += n;
       const int row = item % p.tc_groups * p.tc_rows + (pair ? w * kTcRows : 0) + r;
       const bool live = row < R, any_live = row - lane < R, half_live = row - r < R;
@@ -939,7 +929,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) tc_kernel(const AttnDev p) {
         if (!ok) break;
         tc_after();
         if (any_live) {
-          const int valid = line.prefix - (first + j) * kTcKeys;
+          const int valid = prefix - (first + j) * kTcKeys;
           const uint32_t s = s_of(w, i) + lanes;
           uint32_t x[2][32];
           tm_ld32(s, x[0]);
@@ -958,7 +948,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) tc_kernel(const AttnDev p) {
           if (j == j0) {
             m = top;
           } else {
-            const bool grow = top > m + kTcGrow;
+            const bool grow = top > m + kGrow;
             if (__any_sync(0xffffffffu, grow)) {
               // O can be changed once the half's P V so far are complete
               ok = bar_wait_all(&sh, &sh.o_full[w], (done - 1) & 1, p.status);
@@ -1006,7 +996,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) tc_kernel(const AttnDev p) {
         tc_after();
       }
       if (any_live) {
-        const long long slot = (c + item) * 2 + w;
+        const long long slot = (c + item) * 2ll + w;
         for (int q = 0; q < D / 32; ++q) {
           uint32_t x[32];
           if (some) {
@@ -1028,7 +1018,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) tc_kernel(const AttnDev p) {
   }
   __syncthreads();
   pdl_wait();
-  if (warp == 12) {
+  if (warp == 10) {
     tc_after();
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tm) : "memory");
@@ -1045,60 +1035,50 @@ constexpr int kJoinRows = 8;
 constexpr int kJoinThreads = 512;
 constexpr int kJoinMax = 512;  // partials of a row whose weights are kept at a time
 template <class T, int D>
-__global__ void __launch_bounds__(kJoinThreads) join_kernel(const AttnDev p, int N, int tc_n) {
-  extern __shared__ int sum[];
-  __shared__ int red[kJoinThreads / 32];
+__global__ void __launch_bounds__(kJoinThreads) join_kernel(const AttnDev p) {
   __shared__ float w_s[kJoinMax][kJoinRows], m_s[kJoinThreads], l_s[kJoinThreads];
   __shared__ float4 a_s[3][D / 4][kJoinRows];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, ri = lane % kJoinRows;
   const int d0 = (warp & 3) * (D / 16) + lane / kJoinRows, part = warp >> 2;
   constexpr int kGroups = D / 64;  // element groups of a lane
   pdl_wait();
-  const Line line = make_line(p, N, sum, red);
-  const TcLine tc = tc_line(p, p.tc_rows ? line.prefix : 0, tc_n);
-  const double inv_own = line.total > 0 ? 1.0 / (double)line.total : 0.0, inv_tc = tc.total > 0 ? 1.0 / (double)tc.total : 0.0;
-  const int R = p.B * p.T * p.G, blocks = (R + kJoinRows - 1) / kJoinRows;
-  for (int x = blockIdx.x; x < blocks * p.nkv; x += gridDim.x) {
-    const int kv = x / blocks, first = x % blocks * kJoinRows, row = first + ri;
-    const int g = row % p.G, t = row / p.G % p.T, b = min(row / p.G / p.T, p.B - 1);
-    const bool live = row < R && p.lens[b] >= 0, shared = live && shares(p, b, line.prefix);
-    // the block that owns tile t is the largest c with c * total / N <= t; with
-    // N <= total every block between two that share an item has a part of it
-    auto span = [](long long t0, long long t1, long long n, long long total, double inv, int item, int &slot) {
-      const int c0 = (int)quotient((t0 + 1) * n - 1, total, inv), c1 = (int)quotient(t1 * n - 1, total, inv);
-      slot = c0 + item;
-      return c1 - c0 + 1;
-    };
+  {
+    const int kv = blockIdx.y, first = blockIdx.x * kJoinRows, row = min(first + ri, p.B * p.T * p.G - 1);
+    // (small numbers: a half added, the product with the reciprocal is never off by one)
+    const int u = (int)((row + 0.5f) * p.inv_G), b = (int)((u + 0.5f) * p.inv_T), g = row - u * p.G, t = u - b * p.T;
+    const int how = p.how[b];
+    const bool live = first + ri == row && how >= 0;
     // this row's partials: n1 of the prefix, n2 of its own part
-    int n1 = 0, n2 = 0, slot;
+    int n1 = 0, n2 = 0;
     const float2 *ml1 = p.part_ml, *ml2 = p.part_ml;
     const float4 *o1 = p.part_o, *o2 = p.part_o;
     int ms1 = kRows, rows1 = kRows;
-    if (line.prefix > 0 && (p.tc_rows || p.n_prefix_items)) {
+    if (live && (how & 1)) {
       if (p.tc_rows) {  // (a block's rows are of one group: tc_rows is a multiple of kJoinRows)
-        const int item = kv * p.tc_groups + first / p.tc_rows, in = row % p.tc_rows, r = in % kTcRows;
-        n1 = span((long long)item * tc.tiles, (long long)(item + 1) * tc.tiles, tc.N, tc.total, inv_tc, item, slot);
-        const long long half = slot * 2ll + in / kTcRows;  // pair: this row's half of each slot; else both
+        const int group = first / (2 * kTcRows), in = first % (2 * kTcRows) + ri, r = in % kTcRows;
+        const int item = kv * p.tc_groups + (p.tc_rows == kTcRows ? 0 : group);
+        const int2 w = p.tc_who[item];
+        n1 = w.y - w.x + 1;
+        const long long half = (w.x + item) * 2ll + in / kTcRows;  // pair: this row's half of each slot; else both
         ms1 = 2 * kTcRows;
         if (p.tc_rows == kTcRows) n1 *= 2, ms1 = kTcRows;
         rows1 = kTcRows;
         ml1 = p.tc_ml + half * kTcRows + r;
         o1 = p.tc_o + (half * (D / 4) + d0) * kTcRows + r;
       } else {
-        const int item = kv * (p.n_prefix_items / p.nkv) + first / kRows, r = row % kRows;
-        n1 = span((long long)item * line.prefix_tiles, (long long)(item + 1) * line.prefix_tiles, line.N, line.total, inv_own, item, slot);
-        ml1 = p.part_ml + (long long)slot * kRows + r;
-        o1 = p.part_o + ((long long)slot * (D / 4) + d0) * kRows + r;
+        const int item = kv * p.prefix_tiles + first / kRows, r = row % kRows;
+        const int2 w = p.who[item];
+        n1 = w.y - w.x + 1;
+        ml1 = p.part_ml + (long long)(w.x + item) * kRows + r;
+        o1 = p.part_o + ((long long)(w.x + item) * (D / 4) + d0) * kRows + r;
       }
-      if (!shared) n1 = 0;
     }
-    const int nt = sum[b + 1] - sum[b];
-    if (live && nt > 0) {
-      const int per = p.nkv * p.own_tiles, w = t * p.G + g, k = kv * p.own_tiles + w / kRows, r = w % kRows;
-      const long long t0 = line.own0 + (long long)sum[b] * per + (long long)k * nt;
-      n2 = span(t0, t0 + nt, line.N, line.total, inv_own, p.n_prefix_items + b * per + k, slot);
-      ml2 = p.part_ml + (long long)slot * kRows + r;
-      o2 = p.part_o + ((long long)slot * (D / 4) + d0) * kRows + r;
+    if (live && (how & 2)) {
+      const int x = t * p.G + g, item = p.n_prefix_items + (b * p.nkv + kv) * p.own_tiles + x / kRows, r = x % kRows;
+      const int2 w = p.who[item];
+      n2 = w.y - w.x + 1;
+      ml2 = p.part_ml + (long long)(w.x + item) * kRows + r;
+      o2 = p.part_o + ((long long)(w.x + item) * (D / 4) + d0) * kRows + r;
     }
     // ---- the row's maximum and sum: thread 8 k + i looks at partials k, k + 64, ... of row i
     const int n = n1 + n2;
@@ -1176,7 +1156,6 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const AttnDev p, int
       if (p.lse && d0 == 0)
         p.lse[((long long)b * p.T + t) * p.nq + kv * p.G + g] = L == 0.f ? -INFINITY : (M + log2f(L)) * 0.6931471805599453f;
     }
-    __syncthreads();
   }
 }
 
@@ -1188,10 +1167,11 @@ int check(const mk_attn_shared_args *a) {
       a->n_q_heads / a->n_kv_heads > 16 || a->n_tokens > 16 || (int64_t)a->batch * a->n_tokens > kMaxRowsB ||
       a->n_q_heads > 1024)
     return MK_ERR_UNSUPPORTED_SHAPE;
-  // (tiles of a whole batch are counted in 32 bits)
-  if ((int64_t)a->batch * ((int64_t)a->table_width * a->page / kKeys + 1) >= 1ll << 31) return MK_ERR_INVALID_ARG;
-  if ((int64_t)a->table_width * a->page >= (1ll << 31) - 64 || (int64_t)a->n_prefix_pages * a->page >= (1ll << 31) - 64)
-    return MK_ERR_INVALID_ARG;
+  const int64_t own = (int64_t)a->table_width * a->page, pre = (int64_t)a->n_prefix_pages * a->page;
+  if (own >= (1ll << 31) - 64 || pre >= (1ll << 31) - 64) return MK_ERR_INVALID_ARG;
+  // the work of a whole call is counted in 32 bits, in units of kUnit positions
+  const int64_t rows = (int64_t)a->batch * a->n_tokens * (a->n_q_heads / a->n_kv_heads), tiles = rows / kRows + a->batch;
+  if (a->n_kv_heads * tiles * ((own + pre) / kUnit + 2) >= 1ll << 31) return MK_ERR_INVALID_ARG;
   return MK_OK;
 }
 
@@ -1206,7 +1186,10 @@ void fill(const mk_attn_shared_args *a, AttnDev *d) {
   const int R = d->B * d->T * d->G;
   d->tc_rows = a->n_prefix_pages > 0 && R >= kTcMinRows ? (R <= kTcRows ? kTcRows : 2 * kTcRows) : 0;
   d->tc_groups = d->tc_rows ? (R + d->tc_rows - 1) / d->tc_rows : 0;
-  d->n_prefix_items = a->n_prefix_pages > 0 && !d->tc_rows ? d->nkv * ((R + kRows - 1) / kRows) : 0;
+  d->prefix_tiles = a->n_prefix_pages > 0 && !d->tc_rows ? (R + kRows - 1) / kRows : 0;
+  d->n_prefix_items = d->nkv * d->prefix_tiles;
+  d->inv_G = 1.f / (float)d->G;
+  d->inv_T = 1.f / (float)d->T;
   d->own_tiles = (d->T * d->G + kRows - 1) / kRows;
   d->n_items = d->n_prefix_items + d->B * d->nkv * d->own_tiles;
 }
@@ -1220,19 +1203,18 @@ int sm_count(int *out) {
 
 // The parts of the workspace: bytes of each, in order.
 struct Sizes {
-  int64_t part_o, part_ml, tc_o, tc_ml;
+  int64_t part_o, part_ml, tc_o, tc_ml, who, tc_who, how;
 };
 Sizes sizes_of(const AttnDev &d, int head_dim, int sms) {
-  const int64_t rows = ((int64_t)sms * kBlocksPerSm + d.n_items) * kRows;
+  const int64_t rows = ((int64_t)sms * kBlocksPerSm * kWarps + d.n_items) * kRows;
   const int64_t tc = d.tc_rows ? ((int64_t)sms + d.nkv * d.tc_groups) * 2 * kTcRows : 0;
-  return Sizes{rows * head_dim * 4, rows * 8, tc * head_dim * 4, tc * 8};
+  return Sizes{rows * head_dim * 4, rows * 8, tc * head_dim * 4, tc * 8, 8 * (int64_t)d.n_items, 8 * (int64_t)d.nkv * d.tc_groups, 4 * (int64_t)d.B};
 }
 
 template <class T, int D>
 int launch(const AttnDev &p, int sms, cudaStream_t st) {
-  const size_t smem = smem_tiles<D>() + sizeof(int) * (p.B + 1);
+  const size_t smem = smem_stages<D>() + sizeof(int) * (p.B + 1);
   const int N = sms * kBlocksPerSm;
-  static_assert(smem_tiles<D>() >= kWarps * kRows * (D + 4) * 4, "the warps' partials fit into the tiles");
   // the prefix last: its partials are the larger ones, and the join then finds them in L2
   int rc = serve_code(cudaFuncSetAttribute((const void *)part_kernel<T, D>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem));
   if (!rc) rc = serve_launch(part_kernel<T, D>, dim3(N), kWarps * 32, smem, st, false, 1, p);
@@ -1241,8 +1223,8 @@ int launch(const AttnDev &p, int sms, cudaStream_t st) {
     if (!rc) rc = serve_launch(tc_kernel<T, D>, dim3(sms), kTcThreads, tc_smem<D>(), st, true, 1, p);
   }
   if (rc) return rc;
-  const int grid = std::min((p.B * p.T * p.G + kJoinRows - 1) / kJoinRows * p.nkv, sms * 4);
-  return serve_launch(join_kernel<T, D>, dim3(grid), kJoinThreads, sizeof(int) * (p.B + 1), st, true, 1, p, N, sms);
+  const dim3 grid((p.B * p.T * p.G + kJoinRows - 1) / kJoinRows, p.nkv);
+  return serve_launch(join_kernel<T, D>, grid, kJoinThreads, 0, st, true, 1, p);
 }
 
 }  // namespace
@@ -1257,7 +1239,7 @@ extern "C" int64_t mk_attn_shared_workspace_bytes(const mk_attn_shared_args *a) 
   int sms = 0;
   if (sm_count(&sms)) return 0;
   const Sizes z = sizes_of(d, a->head_dim, sms);
-  return z.part_o + z.part_ml + z.tc_o + z.tc_ml;
+  return z.part_o + z.part_ml + z.tc_o + z.tc_ml + z.who + z.tc_who + z.how;
 }
 
 extern "C" int mk_attn_shared(const mk_attn_shared_args *a, void *workspace, void *stream) {
@@ -1297,6 +1279,7 @@ extern "C" int mk_attn_shared(const mk_attn_shared_args *a, void *workspace, voi
   d.page = a->page;
   d.n_pages = a->n_pages;
   d.page_shift = (a->page & (a->page - 1)) == 0 ? __builtin_ctz((unsigned)a->page) : -1;
+  d.page_units = a->page % kUnit == 0;
   d.n_prefix_pages = a->n_prefix_pages;
   d.table_width = a->table_width;
   // (never 0, so that a masked score stays -infinity)
@@ -1306,10 +1289,18 @@ extern "C" int mk_attn_shared(const mk_attn_shared_args *a, void *workspace, voi
   if ((rc = sm_count(&sms))) return rc;
   const Sizes z = sizes_of(d, a->head_dim, sms);
   char *w = (char *)workspace;
-  d.part_o = (float4 *)w;
-  d.tc_o = (float4 *)(w + z.part_o);
-  d.part_ml = (float2 *)(w + z.part_o + z.tc_o);
-  d.tc_ml = (float2 *)(w + z.part_o + z.tc_o + z.part_ml);
+  auto part = [&](int64_t bytes) {  // the sizes are multiples of 16, but for the last ones' of 8 and 4
+    char *x = w;
+    w += bytes;
+    return x;
+  };
+  d.part_o = (float4 *)part(z.part_o);
+  d.tc_o = (float4 *)part(z.tc_o);
+  d.part_ml = (float2 *)part(z.part_ml);
+  d.tc_ml = (float2 *)part(z.tc_ml);
+  d.who = (int2 *)part(z.who);
+  d.tc_who = (int2 *)part(z.tc_who);
+  d.how = (int *)part(z.how);
   cudaStream_t st = (cudaStream_t)stream;
   if (a->dtype == MK_DTYPE_BF16)
     return a->head_dim == 64 ? launch<__nv_bfloat16, 64>(d, sms, st) : launch<__nv_bfloat16, 128>(d, sms, st);

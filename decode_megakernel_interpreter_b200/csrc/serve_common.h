@@ -5,6 +5,8 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <type_traits>
+
 #include "../../include/mk_serve.h"
 
 namespace mk {
@@ -42,7 +44,7 @@ int serve_launch(void (*fn)(A...), dim3 grid, int threads, size_t smem, cudaStre
   }
   cfg.attrs = at;
   cfg.numAttrs = (unsigned)n;
-  return serve_code(cudaLaunchKernelEx(&cfg, fn, static_cast<A>(args)...));
+  return serve_code(cudaLaunchKernelEx(&cfg, fn, static_cast<std::remove_const_t<A>>(args)...));
 }
 
 inline bool aligned_to(const void *p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }

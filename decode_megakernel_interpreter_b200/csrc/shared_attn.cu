@@ -10,6 +10,7 @@
 // A sequence one of whose queries ends inside the prefix does not share it:
 // its whole length is then its own part, so that the shared part has no masks
 // but the prefix's end.
+#include <cuda.h>  // CUtensorMap (types only: the encoder is looked up at run time)
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -58,6 +59,7 @@ struct AttnDev {
   // the prefix on the tensor cores (tc_rows > 0; n_prefix_items is 0 then):
   // items [kv head][group of tc_rows rows]
   int tc_rows, tc_groups;
+  int box;         // rows of a tensor copy of K/V (0: none)
   float4 *tc_o;    // [slot][half][d / 4][kTcRows]
   float2 *tc_ml;   // [slot][half][kTcRows]
 };
@@ -539,10 +541,13 @@ __global__ void __launch_bounds__(kWarps * 32, kBlocksPerSm) part_kernel(const A
 //   tc_rows = 256: the halves take 128 rows each and read the same K/V tiles;
 //   tc_rows = 128: both take the same rows, and every other K/V tile.
 // Each half has two S of 64 positions: the tensor cores fill one while the
-// softmax works on the other.  Two warps copy the K/V tiles (16 bytes a time,
-// rows from the page list) into a ring in the order they are needed, and a
-// warp for each half issues its matrix instructions (one warp for both spent
-// longer on the waits and descriptors than the instructions took).
+// softmax works on the other.  K/V tiles come into a ring in the order they are
+// needed, by tensor copies of the parts of a tile that lie in one page where
+// pages are multiples of 16 positions, else by two warps 16 bytes a time, as is
+// the prefix's last tile if it is not full (that path alone kept the tensor
+// cores waiting: 42 us for 8 heads x 32768 positions x 128).  A warp for each
+// half issues its matrix instructions (one warp for both spent longer on the
+// waits and descriptors than the instructions took).
 // P takes S's place in tensor memory, rounded to the operands' type: half a
 // step (2^-8 or 2^-11) of each weight, as the output's own rounding.
 
@@ -690,6 +695,16 @@ __device__ __forceinline__ bool bar_wait(TcShared *sh, uint64_t *b, uint32_t par
 __device__ __forceinline__ bool bar_wait_all(TcShared *sh, uint64_t *b, uint32_t parity, int32_t *status) {
   return __all_sync(0xffffffffu, bar_wait(sh, b, parity, status));
 }
+__device__ __forceinline__ void bar_expect(uint64_t *b, uint32_t bytes) {
+  asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(smem_addr(b)), "r"(bytes) : "memory");
+}
+// A box of K or V: 64 elements from x on, of the map's number of rows.
+__device__ __forceinline__ void tensor_copy(const CUtensorMap *map, uint32_t dst, int x, int row, int kv, int page, uint64_t *b) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(dst),
+      "l"(map), "r"(x), "r"(row), "r"(kv), "r"(page), "r"(smem_addr(b))
+      : "memory");
+}
 // Arrive on b when this thread's copies so far have landed.
 __device__ __forceinline__ void cp_arrive(uint64_t *b) {
   asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_addr(b)) : "memory");
@@ -701,7 +716,6 @@ struct TcOrder {
   int n, ahead;
   __device__ __forceinline__ int k_at(int j) const { return j < ahead ? j : 2 * j - ahead + 1; }
   __device__ __forceinline__ int v_at(int j) const { return j < n - ahead ? ahead + 2 * j : n + j; }
-  __device__ __forceinline__ bool is_v(int e) const { return e >= ahead && (e >= 2 * n - ahead || !((e - ahead) & 1)); }
 };
 
 // The blocks' line of tiles.
@@ -713,7 +727,8 @@ struct TcLine {
 };
 
 template <class T, int D>
-__global__ void __launch_bounds__(kTcThreads, 1) tc_kernel(const AttnDev p) {
+__global__ void __launch_bounds__(kTcThreads, 1)
+    tc_kernel(const AttnDev p, const __grid_constant__ CUtensorMap k_map, const __grid_constant__ CUtensorMap v_map) {
   extern __shared__ char sm_raw[];
   __shared__ TcShared sh;
   constexpr int kRing = tc_ring<D>();
@@ -761,39 +776,70 @@ __global__ void __launch_bounds__(kTcThreads, 1) tc_kernel(const AttnDev p) {
   if (warp >= 8 && warp < 10) {
     // ---------------- copies: warp w of the two takes rows 32 w .. 32 w + 31
     // of every tile, 16 at a time
-    int g = 0;  // ring entries begun
+    int slot = 0;         // of the ring
+    uint32_t phase = 1;   // of its `empty`: every slot is free at first
     bool ok = true;
     const int row = (warp - 8) * 32, ch = lane % (D / 8), r0 = lane / (D / 8);
+    // Tensor copies take the box rows of a page at a time, 1, 2 or 4 to a tile.
+    // Lane i knows the page of the i-th of the next 32 (of K, and of V).
+    const int shift = p.box == 64 ? 0 : p.box == 32 ? 1 : 2, boxes = 1 << shift, tiles_mask = (32 >> shift) - 1;
+    const int box_row = (lane & (boxes - 1)) * p.box;
+    const uint32_t box_at = box_row * 128;
+    auto step = [&]() {
+      if (++slot == kRing) {
+        slot = 0;
+        phase ^= 1;
+      }
+    };
     for (int t0 = t_begin; ok && t0 < t_end;) {
       const int item = t0 / line.tiles, first = t0 % line.tiles, n = min(t_end - t0, line.tiles - first), kv = item / p.tc_groups;
       t0 += n;
-      // Pages: where 16 rows are in one page, lane i looks up those of tile j + i
-      // for the next 32 tiles; else a lane looks up that of one row, each time.
-      auto look_up = [&](int j) {
-        const int pos = p.page_units ? (first + j + lane) * kTcKeys + row : (first + j) * kTcKeys + row + (lane & 15);
-        return make_int2(pos < prefix ? p.prefix_pages[page_index(p, pos)] : 0,
-                         pos + 16 < prefix ? p.prefix_pages[page_index(p, pos + 16)] : 0);
-      };
-      const TcOrder order{n, min(dist, n)};
-      int j_of[2] = {0, 0};  // the next K, the next V
-      int2 pages[2] = {};
-      for (int e = 0; e < 2 * n; ++e) {
-        const bool is_v = order.is_v(e);
-        const int slot = g % kRing, j = is_v ? j_of[1]++ : j_of[0]++;
-        int2 pg = is_v ? pages[1] : pages[0];
-        if (!p.page_units || j % 32 == 0) pg = look_up(j);
-        if (is_v) pages[1] = pg;
-        else pages[0] = pg;
-        if (p.page_units) pg = make_int2(__shfl_sync(0xffffffffu, pg.x, j % 32), __shfl_sync(0xffffffffu, pg.y, j % 32));
-        if (g >= kRing) ok = bar_wait_all(&sh, &sh.empty[slot], ((g / kRing) & 1) ^ 1, p.status);
-        if (!ok) break;
+      const int ahead = min(dist, n);
+      int k_next = 0, v_next = 0, k_pages = 0, v_pages = 0;
+      while (v_next < n) {  // (the order of TcOrder)
+        const bool is_v = k_next == n || k_next - v_next >= ahead;
+        const int j = is_v ? v_next++ : k_next++;
+        const int pos0 = (first + j) * kTcKeys;
         const uint32_t dst = ring + slot * tc_tile<D>();
+        uint64_t *full = &sh.full[slot];
+        if (p.box && pos0 + kTcKeys <= prefix) {
+          int pages = is_v ? v_pages : k_pages;
+          if ((j & tiles_mask) == 0) {
+            const int pos = pos0 + lane * p.box;
+            pages = pos < prefix ? p.prefix_pages[page_index(p, pos)] : 0;
+            if (is_v) v_pages = pages;
+            else k_pages = pages;
+          }
+          int pg = __shfl_sync(0xffffffffu, pages, (j & tiles_mask) << shift | (lane & (boxes - 1)));
+          ok = bar_wait_all(&sh, &sh.empty[slot], phase, p.status);
+          if (!ok) break;
+          if (warp == 8 && lane == 0) bar_expect(full, tc_tile<D>());
+          else bar_arrive(full);
+          __syncwarp();
+          if (warp == 8 && lane < boxes) {
+            if ((unsigned)pg >= (unsigned)p.n_pages) {
+              report(p.status, MK_ERR_DEVICE_INPUT);
+              pg = 0;
+            }
+            const int pos = pos0 + box_row, in = pos - page_index(p, pos) * p.page;
+#pragma unroll
+            for (int x = 0; x < D / 64; ++x)
+              tensor_copy(is_v ? &v_map : &k_map, dst + x * (kTcKeys * 128) + box_at, x * 64, in, kv, pg, full);
+          }
+          step();
+          continue;
+        }
+        ok = bar_wait_all(&sh, &sh.empty[slot], phase, p.status);
+        if (!ok) break;
         const char *src = is_v ? p.v : p.k;
-        const int pos = (first + j) * kTcKeys + row;
-        copy_rows<D, false, 128>(p, src, src, kv, pos, 0, prefix, p.page_units, pg.x, dst, tc_at(kTcKeys, row + r0, ch), 0);
-        copy_rows<D, false, 128>(p, src, src, kv, pos + 16, 0, prefix, p.page_units, pg.y, dst, tc_at(kTcKeys, row + 16 + r0, ch), 0);
-        cp_arrive(&sh.full[slot]);
-        ++g;
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+          const int pos = pos0 + row + x * 16, at = pos + (p.page_units ? 0 : lane & 15);
+          copy_rows<D, false, 128>(p, src, src, kv, pos, 0, prefix, p.page_units, at < prefix ? p.prefix_pages[page_index(p, at)] : 0,
+                                   dst, tc_at(kTcKeys, row + x * 16 + r0, ch), 0);
+        }
+        cp_arrive(full);
+        step();
       }
     }
     cp_commit();
@@ -940,44 +986,50 @@ __global__ void __launch_bounds__(kTcThreads, 1) tc_kernel(const AttnDev p) {
             for (int e = 0; e < kTcKeys; ++e)
               if (e >= valid) x[e / 32][e % 32] = 0xff800000u;  // -infinity
           }
-          float t[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+          // The weights are first taken with the maximum so far, while this
+          // tile's own is found; where that has grown too much (and in an
+          // item's first tile), once more.
+          uint32_t h[32];
+          unsigned long long sum;
+          for (;;) {
+            const float b = m == -INFINITY ? 0.f : m;
+            const unsigned long long scale = pack2(p.scale2, p.scale2), minus = pack2(-b, -b);
+            float t[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+            sum = 0ull;
 #pragma unroll
-          for (int e = 0; e < kTcKeys; ++e) t[e & 3] = fmaxf(t[e & 3], __uint_as_float(x[e / 32][e % 32]));
-          float top = fmaxf(fmaxf(t[0], t[1]), fmaxf(t[2], t[3]));
-          top = top == -INFINITY ? top : top * p.scale2;
-          if (j == j0) {
-            m = top;
-          } else {
-            const bool grow = top > m + kGrow;
-            if (__any_sync(0xffffffffu, grow)) {
-              // O can be changed once the half's P V so far are complete
-              ok = bar_wait_all(&sh, &sh.o_full[w], (done - 1) & 1, p.status);
-              if (!ok) break;
-              tc_after();
-              const float f = grow ? exp2_(m - top) : 1.f;
-              if (grow) m = top;
-              l *= f;
-              for (int q = 0; q < D / 16; ++q) {
-                uint32_t y[16];
-                tm_ld16(o_of(w) + lanes + q * 16, y);
-                tm_wait_ld();
+            for (int e = 0; e < kTcKeys; e += 2) {
+              const float x0 = __uint_as_float(x[e / 32][e % 32]), x1 = __uint_as_float(x[e / 32][e % 32 + 1]);
+              t[e & 2] = fmaxf(t[e & 2], x0);
+              t[(e & 2) + 1] = fmaxf(t[(e & 2) + 1], x1);
+              const float2 y = unpack2(fma2(pack2(x0, x1), scale, minus));
+              const float e0 = exp2_(y.x), e1 = exp2_(y.y);
+              sum = add2(sum, pack2(e0, e1));
+              h[e / 2] = Num<T>::pack(e0, e1);
+            }
+            const float top = fmaxf(fmaxf(t[0], t[1]), fmaxf(t[2], t[3])) * p.scale2;
+            const bool grow = top > (m == -INFINITY ? m : m + kGrow);
+            if (!__any_sync(0xffffffffu, grow)) break;
+            if (j == j0) {
+              m = fmaxf(m, top);
+              continue;
+            }
+            // O can be changed once the half's P V so far are complete
+            ok = bar_wait_all(&sh, &sh.o_full[w], (done - 1) & 1, p.status);
+            if (!ok) break;
+            tc_after();
+            const float f = grow ? exp2_(m - top) : 1.f;
+            if (grow) m = top;
+            l *= f;
+            for (int q = 0; q < D / 16; ++q) {
+              uint32_t y[16];
+              tm_ld16(o_of(w) + lanes + q * 16, y);
+              tm_wait_ld();
 #pragma unroll
-                for (int e = 0; e < 16; ++e) y[e] = __float_as_uint(__uint_as_float(y[e]) * f);
-                tm_st16(o_of(w) + lanes + q * 16, y);
-              }
+              for (int e = 0; e < 16; ++e) y[e] = __float_as_uint(__uint_as_float(y[e]) * f);
+              tm_st16(o_of(w) + lanes + q * 16, y);
             }
           }
-          const float b = m == -INFINITY ? 0.f : m;
-          const unsigned long long scale = pack2(p.scale2, p.scale2), minus = pack2(-b, -b);
-          unsigned long long sum = 0ull;
-          uint32_t h[32];
-#pragma unroll
-          for (int e = 0; e < kTcKeys; e += 2) {
-            const float2 y = unpack2(fma2(pack2(__uint_as_float(x[e / 32][e % 32]), __uint_as_float(x[e / 32][e % 32 + 1])), scale, minus));
-            const float e0 = exp2_(y.x), e1 = exp2_(y.y);
-            sum = add2(sum, pack2(e0, e1));
-            h[e / 2] = Num<T>::pack(e0, e1);
-          }
+          if (!ok) break;
           tm_st32(s, h);
           const float2 both = unpack2(sum);
           l += both.x + both.y;
@@ -1036,7 +1088,7 @@ constexpr int kJoinThreads = 512;
 constexpr int kJoinMax = 512;  // partials of a row whose weights are kept at a time
 template <class T, int D>
 __global__ void __launch_bounds__(kJoinThreads) join_kernel(const AttnDev p) {
-  __shared__ float w_s[kJoinMax][kJoinRows], m_s[kJoinThreads], l_s[kJoinThreads];
+  __shared__ float w_s[kJoinMax][kJoinRows], m_s[kJoinThreads / 32][kJoinRows], l_s[kJoinThreads / 32][kJoinRows];
   __shared__ float4 a_s[3][D / 4][kJoinRows];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, ri = lane % kJoinRows;
   const int d0 = (warp & 3) * (D / 16) + lane / kJoinRows, part = warp >> 2;
@@ -1087,37 +1139,34 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const AttnDev p) {
       return *y;
     };
     float M = -INFINITY, L = 0.f;
+#pragma unroll 1
     for (int i = tid / kJoinRows; i < n; i += kJoinThreads / kJoinRows) {
       const float2 y = ml_of(i);
-      const float m = y.y == 0.f ? -INFINITY : y.x, top = fmaxf(M, m), base = top == -INFINITY ? 0.f : top;
-      L = L * exp2_(M - base) + (y.y == 0.f ? 0.f : y.y * exp2_(m - base));
-      M = top;
+      if (y.y != 0.f) M = fmaxf(M, y.x);
     }
-    auto meet = [&](float m, float l) {
-      const float top = fmaxf(M, m), base = top == -INFINITY ? 0.f : top;
-      L = L * exp2_(M - base) + l * exp2_(m - base);
-      M = top;
-    };
 #pragma unroll
-    for (int o = 8; o < 32; o <<= 1) meet(__shfl_xor_sync(0xffffffffu, M, o), __shfl_xor_sync(0xffffffffu, L, o));
-    if (lane < kJoinRows) m_s[warp * kJoinRows + ri] = M, l_s[warp * kJoinRows + ri] = L;
+    for (int o = 8; o < 32; o <<= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+    if (lane < kJoinRows) m_s[warp][ri] = M;
     __syncthreads();
-    M = -INFINITY, L = 0.f;
-    for (int w = 0; w < min(kJoinThreads / 32, (n + 3) / 4); ++w) meet(m_s[w * kJoinRows + ri], l_s[w * kJoinRows + ri]);
+#pragma unroll
+    for (int w = 0; w < kJoinThreads / 32; ++w) M = fmaxf(M, m_s[w][ri]);
     const float base = M == -INFINITY ? 0.f : M;
     // ---- the elements
     float4 a[kGroups];
 #pragma unroll
     for (int k = 0; k < kGroups; ++k) a[k] = make_float4(0.f, 0.f, 0.f, 0.f);
     const int n_max = __reduce_max_sync(0xffffffffu, n);  // (of the block: every warp has the same rows)
+#pragma unroll 1
     for (int i0 = 0; i0 < n_max; i0 += kJoinMax) {
       for (int i = i0 + tid / kJoinRows; i < min(n, i0 + kJoinMax); i += kJoinThreads / kJoinRows) {
         const float2 y = ml_of(i);
-        w_s[i - i0][ri] = y.y == 0.f ? 0.f : exp2_(y.x - base);
+        const float f = y.y == 0.f ? 0.f : exp2_(y.x - base);
+        w_s[i - i0][ri] = f;
+        L += f * y.y;
       }
       __syncthreads();
       auto add = [&](const float4 *o, long long os, int rows, int from, int to) {  // partials from, from + 4, ... of this row
-#pragma unroll 4
+#pragma unroll 6
         for (int i = from; i < to; i += 4) {
           const float f = w_s[i - i0][ri];
 #pragma unroll
@@ -1133,13 +1182,19 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const AttnDev p) {
       const int end = min(n, i0 + kJoinMax), cut = min(max(n1, i0), end), own = cut + ((part - cut) & 3);
       add(o1, (long long)ms1 * (D / 4), rows1, i0 + part, cut);
       add(o2 - (long long)n1 * kRows * (D / 4), (long long)kRows * (D / 4), kRows, own, end);
-      __syncthreads();
+      if (i0 + kJoinMax < n_max) __syncthreads();
     }
+#pragma unroll
+    for (int o = 8; o < 32; o <<= 1) L += __shfl_xor_sync(0xffffffffu, L, o);
+    if (lane < kJoinRows) l_s[warp][ri] = L;
 #pragma unroll
     for (int k = 0; k < kGroups; ++k)
       if (part > 0) a_s[part - 1][d0 + 4 * k][ri] = a[k];
     __syncthreads();
     if (part == 0 && live) {
+      L = 0.f;
+#pragma unroll
+      for (int w = 0; w < kJoinThreads / 32; ++w) L += l_s[w][ri];
       const float inv = L == 0.f ? 0.f : 1.f / L;  // (a NaN stays)
       char *op = p.out + b * p.o_bs + t * p.o_ts + (kv * p.G + g) * p.o_hs + d0 * 8;
 #pragma unroll
@@ -1201,6 +1256,33 @@ int sm_count(int *out) {
   return serve_code(e);
 }
 
+// The tensor map of K or V: boxes of 64 elements x `rows` positions of one head
+// of one page, with the 128-byte swizzle.
+bool make_map(CUtensorMap *map, const mk_attn_shared_args *a, const void *x, int rows) {
+  typedef CUresult (*Encode)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *, const cuuint64_t *,
+                             const cuuint32_t *, const cuuint32_t *, CUtensorMapInterleave, CUtensorMapSwizzle,
+                             CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+  static const Encode encode = [] {
+    void *f = nullptr;
+    cudaDriverEntryPointQueryResult how;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &how) != cudaSuccess ||
+        how != cudaDriverEntryPointSuccess) {
+      cudaGetLastError();
+      f = nullptr;
+    }
+    return (Encode)f;
+  }();
+  if (!encode) return false;
+  const cuuint64_t dims[4] = {(cuuint64_t)a->head_dim, (cuuint64_t)a->page, (cuuint64_t)a->n_kv_heads, (cuuint64_t)a->n_pages};
+  const cuuint64_t strides[3] = {2 * (cuuint64_t)a->row_stride, 2 * (cuuint64_t)a->kv_head_stride, 2 * (cuuint64_t)a->page_stride};
+  for (cuuint64_t t : strides)
+    if (t == 0 || t >= 1ull << 40) return false;
+  const cuuint32_t box[4] = {64, (cuuint32_t)rows, 1, 1}, one[4] = {1, 1, 1, 1};
+  return encode(map, a->dtype == MK_DTYPE_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 4,
+                const_cast<void *>(x), dims, strides, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 // The parts of the workspace: bytes of each, in order.
 struct Sizes {
   int64_t part_o, part_ml, tc_o, tc_ml, who, tc_who, how;
@@ -1212,7 +1294,7 @@ Sizes sizes_of(const AttnDev &d, int head_dim, int sms) {
 }
 
 template <class T, int D>
-int launch(const AttnDev &p, int sms, cudaStream_t st) {
+int launch(const AttnDev &p, const CUtensorMap (&maps)[2], int sms, cudaStream_t st) {
   const size_t smem = smem_stages<D>() + sizeof(int) * (p.B + 1);
   const int N = sms * kBlocksPerSm;
   // the prefix last: its partials are the larger ones, and the join then finds them in L2
@@ -1220,7 +1302,7 @@ int launch(const AttnDev &p, int sms, cudaStream_t st) {
   if (!rc) rc = serve_launch(part_kernel<T, D>, dim3(N), kWarps * 32, smem, st, false, 1, p);
   if (!rc && p.tc_rows) {
     rc = serve_code(cudaFuncSetAttribute((const void *)tc_kernel<T, D>, cudaFuncAttributeMaxDynamicSharedMemorySize, tc_smem<D>()));
-    if (!rc) rc = serve_launch(tc_kernel<T, D>, dim3(sms), kTcThreads, tc_smem<D>(), st, true, 1, p);
+    if (!rc) rc = serve_launch(tc_kernel<T, D>, dim3(sms), kTcThreads, tc_smem<D>(), st, true, 1, p, maps[0], maps[1]);
   }
   if (rc) return rc;
   const dim3 grid((p.B * p.T * p.G + kJoinRows - 1) / kJoinRows, p.nkv);
@@ -1301,8 +1383,13 @@ extern "C" int mk_attn_shared(const mk_attn_shared_args *a, void *workspace, voi
   d.who = (int2 *)part(z.who);
   d.tc_who = (int2 *)part(z.tc_who);
   d.how = (int *)part(z.how);
+  CUtensorMap maps[2] = {};
+  if (d.tc_rows && d.page_units) {
+    const int rows = a->page % 64 == 0 ? 64 : a->page % 32 == 0 ? 32 : 16;
+    if (make_map(&maps[0], a, a->k, rows) && make_map(&maps[1], a, a->v, rows)) d.box = rows;
+  }
   cudaStream_t st = (cudaStream_t)stream;
   if (a->dtype == MK_DTYPE_BF16)
-    return a->head_dim == 64 ? launch<__nv_bfloat16, 64>(d, sms, st) : launch<__nv_bfloat16, 128>(d, sms, st);
-  return a->head_dim == 64 ? launch<__half, 64>(d, sms, st) : launch<__half, 128>(d, sms, st);
+    return a->head_dim == 64 ? launch<__nv_bfloat16, 64>(d, maps, sms, st) : launch<__nv_bfloat16, 128>(d, maps, sms, st);
+  return a->head_dim == 64 ? launch<__half, 64>(d, maps, sms, st) : launch<__half, 128>(d, maps, sms, st);
 }

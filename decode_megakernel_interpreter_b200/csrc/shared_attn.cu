@@ -25,9 +25,11 @@ namespace {
 
 constexpr int kRows = 16;    // query rows of an item (one m16 matrix instruction)
 constexpr int kUnit = 16;    // positions that a warp takes at a time
-constexpr int kWarps = 4;    // of a block of the partial kernel, each on its own
+constexpr int kWarps = 12;   // of a block; one block an SM
 constexpr int kStages = 2;   // units of a warp in shared memory
-constexpr int kBlocksPerSm = 3;  // of the partial kernel
+// What beginning and ending an item costs a warp, in units (about 3.5 us against
+// 1.9): without it the warps with many short items were the last by 15 us.
+constexpr int kItemCost = 2;
 constexpr int kMaxRowsB = 1024;
 // A row's maximum only moves when it grows by more than 2^8: until then the
 // weights are at most 2^8, which neither type nor the 32-bit sums mind, and the
@@ -96,15 +98,18 @@ __device__ __forceinline__ bool shares(const AttnDev &p, int n, int prefix) { re
 // Units of the positions [lo, hi): multiples of kUnit, the first and last may
 // lie partly outside.
 __device__ __forceinline__ int units(int lo, int hi) { return hi > lo ? (hi + kUnit - 1) / kUnit - lo / kUnit : 0; }
+// An item's length on the line: its units, and its own cost before them.
+__device__ __forceinline__ int weight(int lo, int hi) { return hi > lo ? units(lo, hi) + kItemCost : 0; }
 
-// The line of the partial kernel's items, in units: prefix items, then own
-// items; sum[b] = units of one own item of each sequence before b.
+// The line of the small items, by weight: prefix items (where the prefix does
+// not go to the tensor cores), then own items; sum[b] = weights of one own item
+// of each sequence before b.
 struct Line {
-  int prefix, prefix_units, own0;  // own0: where the own items begin
+  int prefix_weight, own0;  // own0: where the own items begin
   Share share;
-  __device__ __forceinline__ Line(const AttnDev &p, int prefix_, int own_units, int workers)
-      : prefix(prefix_), prefix_units(units(0, prefix_)), own0(p.n_prefix_items * prefix_units),
-        share(own0 + own_units * p.nkv * p.own_tiles, workers) {}
+  __device__ __forceinline__ Line(const AttnDev &p, int prefix, int own_weight, int workers)
+      : prefix_weight(weight(0, prefix)), own0(p.n_prefix_items * prefix_weight),
+        share(own0 + own_weight * p.nkv * p.own_tiles, workers) {}
 };
 // sum (B + 1 ints of shared memory) and the prefix's length; called by the whole block.
 __device__ int make_sums(const AttnDev &p, int *sum, int *red) {
@@ -112,7 +117,7 @@ __device__ int make_sums(const AttnDev &p, int *sum, int *red) {
   const int b0 = min((int)threadIdx.x * per, p.B), b1 = min(b0 + per, p.B), prefix = prefix_of(p);
   auto own = [&](int b) {
     const int n = seq_len(p, b);
-    return units(shares(p, n, prefix) ? prefix : 0, n);
+    return weight(shares(p, n, prefix) ? prefix : 0, n);
   };
   int mine = 0;
   for (int b = b0; b < b1; ++b) mine += own(b);
@@ -224,8 +229,8 @@ struct Num<__half> {
   }
 };
 
-// Shared memory of the partial kernel: each warp's stages (a unit's rows of K,
-// then of V); then the line's sums.
+// Shared memory of the small items: each warp's stages (a unit's rows of K, then
+// of V); then the line's sums.
 template <int D>
 constexpr int smem_stage() {
   return 2 * kUnit * D * 2;
@@ -293,18 +298,15 @@ __device__ __forceinline__ void copy_rows(const AttnDev &p, const char *k, const
 // of 16 positions through two stages of shared memory, no barrier.  Such items
 // are small (a sequence's own part, or a prefix with few rows), so what counts
 // is how many of them wait for memory at once: 12 warps an SM, each with the
-// next unit in flight.
+// next unit in flight.  They come before the prefix, whose partials are the
+// larger ones: the join then finds those in L2.
 template <class T, int D>
-__global__ void __launch_bounds__(kWarps * 32, kBlocksPerSm) part_kernel(const AttnDev p) {
-  extern __shared__ __align__(128) char sm[];
-  __shared__ int red[kWarps];
+__device__ __forceinline__ void small_items(const AttnDev &p, char *sm, int *red) {
   int *sum = reinterpret_cast<int *>(sm + smem_stages<D>());
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   constexpr int kHalf = kUnit * D * 2, kStage = 2 * kHalf;
   char *const mine = sm + warp * kStages * kStage;
   const uint32_t mine_a = smem_addr(mine);
-  pdl_wait();
-  pdl_trigger();
   const int prefix = make_sums(p, sum, red);
   const Line line(p, prefix, sum[p.B], gridDim.x * kWarps);
   const int c = warp * gridDim.x + blockIdx.x;  // (neighbours along the line on different SMs)
@@ -317,9 +319,9 @@ __global__ void __launch_bounds__(kWarps * 32, kBlocksPerSm) part_kernel(const A
     int b = -1;                          // own item's sequence
     int item_t0, item_n;
     if (t0 < line.own0) {
-      item = t0 / line.prefix_units;
-      item_t0 = item * line.prefix_units;
-      item_n = line.prefix_units;
+      item = t0 / line.prefix_weight;
+      item_t0 = item * line.prefix_weight;
+      item_n = line.prefix_weight;
       kv = item / p.prefix_tiles;
       row0 = item % p.prefix_tiles * kRows;
       n_rows = min(kRows, p.B * p.T * p.G - row0);
@@ -344,11 +346,13 @@ __global__ void __launch_bounds__(kWarps * 32, kBlocksPerSm) part_kernel(const A
       hi = seq_len(p, b);
       lo = shares(p, hi, prefix) ? prefix : 0;
     }
-    const int first = t0 - item_t0, n = min(t_end, item_t0 + item_n) - t0;
-    t0 += n;
+    const int item_end = item_t0 + item_n, begin = max(t0, item_t0 + kItemCost), first = begin - item_t0 - kItemCost;
+    const int n = min(t_end, item_end) - begin;
+    t0 = min(t_end, item_end);
+    if (n <= 0) continue;  // (the item's cost alone)
     if (lane == 0) {
       if (first == 0) p.who[item].x = c;
-      if (first + n == item_n) p.who[item].y = c;
+      if (t0 == item_end) p.who[item].y = c;
     }
 
     const int *table = p.table + (long long)b * p.table_width;  // (not used by prefix items)
@@ -555,7 +559,7 @@ constexpr int kTcRows = 128;  // rows of a half
 constexpr int kTcKeys = 64;   // positions of a tile
 // warps 0-3 and 4-7: softmax; 8 and 9: copies; 10 and 11: matrix instructions.
 // (With a thirteenth warp a thread could have 128 registers only.)
-constexpr int kTcThreads = 12 * 32;
+constexpr int kTcThreads = kWarps * 32;
 template <int D>
 constexpr int tc_tile() {
   return kTcKeys * D * 2;
@@ -719,20 +723,36 @@ struct TcOrder {
 };
 
 // The blocks' line of tiles.
+// (An item's beginning and end cost a block as much as about 4 tiles: with that
+// counted, the blocks that take parts of two items end with the others.)
+constexpr int kTcItemCost = 4;
 struct TcLine {
   int tiles;
   Share share;
   __device__ __forceinline__ TcLine(const AttnDev &p, int prefix, int blocks)
-      : tiles((prefix + kTcKeys - 1) / kTcKeys), share(tiles * p.nkv * p.tc_groups, blocks) {}
+      : tiles((prefix + kTcKeys - 1) / kTcKeys), share(tiles > 0 ? (tiles + kTcItemCost) * p.nkv * p.tc_groups : 0, blocks) {}
+  // The next part of a block's share [t0, t_end): false when there is none.
+  __device__ __forceinline__ bool next(int &t0, int t_end, int &item, int &first, int &n) const {
+    while (t0 < t_end) {
+      item = t0 / (tiles + kTcItemCost);
+      const int at = item * (tiles + kTcItemCost), end = min(t_end, at + tiles + kTcItemCost), from = max(t0, at + kTcItemCost);
+      t0 = end;
+      first = from - at - kTcItemCost;
+      n = end - from;
+      if (n > 0) return true;
+    }
+    return false;
+  }
 };
 
 template <class T, int D>
 __global__ void __launch_bounds__(kTcThreads, 1)
-    tc_kernel(const AttnDev p, const __grid_constant__ CUtensorMap k_map, const __grid_constant__ CUtensorMap v_map) {
+    attn_kernel(const AttnDev p, const __grid_constant__ CUtensorMap k_map, const __grid_constant__ CUtensorMap v_map) {
   extern __shared__ char sm_raw[];
   __shared__ TcShared sh;
   constexpr int kRing = tc_ring<D>();
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  __shared__ int red[kWarps];
   const uint32_t base = (smem_addr(sm_raw) + 1023) & ~1023u;
   char *sm = sm_raw + (base - smem_addr(sm_raw));
   const uint32_t ring = base + 2 * kTcRows * D * 2;
@@ -757,14 +777,16 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   }
   if (warp == 10)
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_addr(&sh.tmem)) : "memory");
-  // This kernel starts as blocks of the own parts' kernel end.  It reads
-  // nothing of theirs, and only waits for them before it ends itself.
+  pdl_wait();
   pdl_trigger();
+  small_items<T, D>(p, sm, red);
+  cp_wait<0>();
+  fence_smem_async();  // the tensor copies reuse the small items' stages
   tc_before();
   __syncthreads();
   tc_after();
   const uint32_t tm = sh.tmem;
-  const int prefix = prefix_of(p), c = blockIdx.x;
+  const int prefix = p.tc_rows ? prefix_of(p) : 0, c = blockIdx.x;
   const TcLine line(p, prefix, gridDim.x);
   const int dist = pair ? 2 : 4;               // K tiles that are multiplied ahead of their V
   const int R = p.B * p.T * p.G;
@@ -791,9 +813,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         phase ^= 1;
       }
     };
-    for (int t0 = t_begin; ok && t0 < t_end;) {
-      const int item = t0 / line.tiles, first = t0 % line.tiles, n = min(t_end - t0, line.tiles - first), kv = item / p.tc_groups;
-      t0 += n;
+    for (int t0 = t_begin, item, first, n; ok && line.next(t0, t_end, item, first, n);) {
+      const int kv = item / p.tc_groups;
       const int ahead = min(dist, n);
       int k_next = 0, v_next = 0, k_pages = 0, v_pages = 0;
       while (v_next < n) {  // (the order of TcOrder)
@@ -876,9 +897,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       }
       __syncwarp();
     };
-    for (int t0 = t_begin; ok && t0 < t_end;) {
-      const int item = t0 / line.tiles, first = t0 % line.tiles, n = min(t_end - t0, line.tiles - first);
-      t0 += n;
+    for (int t0 = t_begin, item, first, n; ok && line.next(t0, t_end, item, first, n);) {
       if (w == 0 && lane == 0) {
         if (first == 0) p.tc_who[item].x = c;
         if (first + n == line.tiles) p.tc_who[item].y = c;
@@ -937,9 +956,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     uint32_t s_phase = 0;  // bit i
     int done = 0;          // tiles of this half so far
     bool ok = true;
-    for (int t0 = t_begin; ok && t0 < t_end;) {
-      const int item = t0 / line.tiles, first = t0 % line.tiles, n = min(t_end - t0, line.tiles - first), kv = item / p.tc_groups;
-      t0 += n;
+    for (int t0 = t_begin, item, first, n; ok && line.next(t0, t_end, item, first, n);) {
+      const int kv = item / p.tc_groups;
       const int row = item % p.tc_groups * p.tc_rows + (pair ? w * kTcRows : 0) + r;
       const bool live = row < R, any_live = row - lane < R, half_live = row - r < R;
       const int step = pair ? 1 : 2, j0 = pair ? 0 : w;
@@ -1069,7 +1087,6 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     }
   }
   __syncthreads();
-  pdl_wait();
   if (warp == 10) {
     tc_after();
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
@@ -1224,9 +1241,9 @@ int check(const mk_attn_shared_args *a) {
     return MK_ERR_UNSUPPORTED_SHAPE;
   const int64_t own = (int64_t)a->table_width * a->page, pre = (int64_t)a->n_prefix_pages * a->page;
   if (own >= (1ll << 31) - 64 || pre >= (1ll << 31) - 64) return MK_ERR_INVALID_ARG;
-  // the work of a whole call is counted in 32 bits, in units of kUnit positions
+  // the work of a whole call is counted in 32 bits
   const int64_t rows = (int64_t)a->batch * a->n_tokens * (a->n_q_heads / a->n_kv_heads), tiles = rows / kRows + a->batch;
-  if (a->n_kv_heads * tiles * ((own + pre) / kUnit + 2) >= 1ll << 31) return MK_ERR_INVALID_ARG;
+  if (a->n_kv_heads * tiles * ((own + pre) / kUnit + 2 + 2 * kItemCost) >= 1ll << 31) return MK_ERR_INVALID_ARG;
   return MK_OK;
 }
 
@@ -1288,22 +1305,16 @@ struct Sizes {
   int64_t part_o, part_ml, tc_o, tc_ml, who, tc_who, how;
 };
 Sizes sizes_of(const AttnDev &d, int head_dim, int sms) {
-  const int64_t rows = ((int64_t)sms * kBlocksPerSm * kWarps + d.n_items) * kRows;
+  const int64_t rows = ((int64_t)sms * kWarps + d.n_items) * kRows;
   const int64_t tc = d.tc_rows ? ((int64_t)sms + d.nkv * d.tc_groups) * 2 * kTcRows : 0;
   return Sizes{rows * head_dim * 4, rows * 8, tc * head_dim * 4, tc * 8, 8 * (int64_t)d.n_items, 8 * (int64_t)d.nkv * d.tc_groups, 4 * (int64_t)d.B};
 }
 
 template <class T, int D>
 int launch(const AttnDev &p, const CUtensorMap (&maps)[2], int sms, cudaStream_t st) {
-  const size_t smem = smem_stages<D>() + sizeof(int) * (p.B + 1);
-  const int N = sms * kBlocksPerSm;
-  // the prefix last: its partials are the larger ones, and the join then finds them in L2
-  int rc = serve_code(cudaFuncSetAttribute((const void *)part_kernel<T, D>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem));
-  if (!rc) rc = serve_launch(part_kernel<T, D>, dim3(N), kWarps * 32, smem, st, false, 1, p);
-  if (!rc && p.tc_rows) {
-    rc = serve_code(cudaFuncSetAttribute((const void *)tc_kernel<T, D>, cudaFuncAttributeMaxDynamicSharedMemorySize, tc_smem<D>()));
-    if (!rc) rc = serve_launch(tc_kernel<T, D>, dim3(sms), kTcThreads, tc_smem<D>(), st, true, 1, p, maps[0], maps[1]);
-  }
+  static_assert(smem_stages<D>() + 4 * (kMaxRowsB + 1) + 1024 <= tc_smem<D>(), "the small items' stages and sums fit");
+  int rc = serve_code(cudaFuncSetAttribute((const void *)attn_kernel<T, D>, cudaFuncAttributeMaxDynamicSharedMemorySize, tc_smem<D>()));
+  if (!rc) rc = serve_launch(attn_kernel<T, D>, dim3(sms), kTcThreads, tc_smem<D>(), st, false, 1, p, maps[0], maps[1]);
   if (rc) return rc;
   const dim3 grid((p.B * p.T * p.G + kJoinRows - 1) / kJoinRows, p.nkv);
   return serve_launch(join_kernel<T, D>, grid, kJoinThreads, 0, st, true, 1, p);

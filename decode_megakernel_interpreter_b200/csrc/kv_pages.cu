@@ -467,23 +467,10 @@ size_t pool_bytes(const mk_kv_pool &p) {
 }
 PoolDev dev(const mk_kv_pool &p) { return PoolDev{(char *)p.k, (char *)p.v, p.n_pages, p.page}; }
 
-int sm_count(int *out) {
-  int d = 0;
-  cudaError_t e = cudaGetDevice(&d);
-  if (e == cudaSuccess) e = cudaDeviceGetAttribute(out, cudaDevAttrMultiProcessorCount, d);
-  return serve_code(e);
-}
-
-// A block with `bytes` of page bitmap.
-template <class K>
-int allow_smem(K fn, size_t bytes) {
-  return serve_code(cudaFuncSetAttribute((const void *)fn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes));
-}
-
 // The grid that moves the listed rows (max_jobs: as many as there can be).
 int launch_move(const mk_kv_pool &a, const mk_kv_pool &b, const Job *jobs, const int *count, int n, const int *good,
                 const int *to, const State &s, cudaStream_t st) {
-  int sms = 0, rc = sm_count(&sms);
+  int sms = 0, rc = serve_sms(&sms);
   if (rc) return rc;
   const int row_bytes = a.head_dim * a.elem_bytes;
   const int piece_rows = std::max(1, kPieceBytes / row_bytes);
@@ -527,7 +514,8 @@ extern "C" int mk_kv_resize(const mk_kv_pool *pool, const mk_kv_state *st, const
   cudaStream_t cs = (cudaStream_t)stream;
   const State s = state_of(*st);
   const size_t smem = ((size_t)st->n_pages + 31) / 32 * 4;
-  int rc = smem > 16384 ? allow_smem(resize_kernel, smem) : MK_OK;
+  static std::atomic<uint64_t> allowed;
+  int rc = smem > 16384 ? serve_allow_smem(allowed, (const void *)resize_kernel, kMaxPages / 8) : MK_OK;
   if (!rc) rc = serve_launch(resize_kernel, dim3(1), kMetaThreads, smem, cs, false, 1, s, seqs, lens, n, pool->page, workspace);
   if (rc) return rc;
   const Work w = work_of(workspace);
@@ -553,7 +541,8 @@ extern "C" int mk_kv_compact(const mk_kv_pool *pool, const mk_kv_state *st, void
   const Work w = work_of(workspace);
   int *to = reinterpret_cast<int *>(w.jobs + st->n_pages);
   const size_t smem = ((size_t)st->n_pages + 31) / 32 * 4;
-  int rc = smem > 16384 ? allow_smem(compact_kernel, smem) : MK_OK;
+  static std::atomic<uint64_t> allowed;
+  int rc = smem > 16384 ? serve_allow_smem(allowed, (const void *)compact_kernel, kMaxPages / 8) : MK_OK;
   if (!rc) rc = serve_launch(compact_kernel, dim3(1), kMetaThreads, smem, cs, false, 1, s, to, pool->page, workspace);
   if (rc) return rc;
   return launch_move(*pool, *pool, w.jobs, w.count, st->n_pages, nullptr, to, s, cs);

@@ -7,6 +7,7 @@
 #include <cuda_fp16.h>
 
 #include <algorithm>
+#include <cstring>
 
 #include "serve_common.h"
 
@@ -30,20 +31,31 @@ struct Part {
   int bad;     // a NaN
 };
 
+// Four consecutive logits as 32-bit values.
+__device__ __forceinline__ float4 four(const float *z) {
+  float4 v;
+  asm volatile("ld.global.L1::no_allocate.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "l"(z));
+  return v;
+}
 template <class T>
-struct alignas(16) Vec16 {
-  T x[16 / sizeof(T)];
-};
+__device__ __forceinline__ float4 four(const T *z) {  // 16-bit types
+  uint2 w;
+  asm volatile("ld.global.L1::no_allocate.v2.u32 {%0, %1}, [%2];" : "=r"(w.x), "=r"(w.y) : "l"(z));
+  T x[4];
+  memcpy(x, &w, 8);
+  return make_float4(up(x[0]), up(x[1]), up(x[2]), up(x[3]));
+}
 
-// probs = exp((z - max) / T) / sum.  One read of the logits: a block keeps its
-// slice as 32-bit values in shared memory (kept = 1), first z, then
-// exp((z - m) / T) with its own maximum m, which the rescaling to the row's
-// maximum and sum turns into probabilities.  Slices that do not fit are read
-// again (kept = 0).  Bound by memory: n * vocab reads and writes.
-template <class T>
+// probs = exp((z - max) / T) / sum.  A block of the row's cluster keeps its
+// slice, 4 kN values a thread: first z, then exp((z - m) / T) with its own
+// maximum m, which the rescaling to the row's maximum and sum turns into
+// probabilities.  kN > 0: in registers, so that the row is read once, all loads
+// of a thread at a time, and nothing but maxima and sums goes through shared
+// memory; a vocabulary too large for that (kN = 0) is read three times.  Bound
+// by memory: each logit read and each probability written once.
+template <class T, int kN>
 __global__ void __launch_bounds__(kProbThreads) probs_kernel(const T *logits, long long ls, const float *temperature,
-                                                             float *probs, long long ps, int vocab, int per, int kept) {
-  extern __shared__ __align__(16) float e_s[];
+                                                             float *probs, long long ps, int vocab, int per) {
   __shared__ Part part, warp_part[kProbThreads / 32];
   cg::cluster_group cl = cg::this_cluster();
   const int C = cl.num_blocks(), rank = cl.block_rank();
@@ -53,73 +65,80 @@ __global__ void __launch_bounds__(kProbThreads) probs_kernel(const T *logits, lo
   float *out = probs + row * ps + v0;
   const float t = temperature ? temperature[row] : 1.f;
   const bool greedy = t == 0.f;
-  constexpr int kV = 16 / sizeof(T);
-  const bool vec = (reinterpret_cast<uintptr_t>(z) & 15) == 0;
+  // Rows that start on 16 (or 8) bytes in both places go four values at a time:
+  // the thread's j-th four are at 4 (512 j + tid); else at 2048 j + 512 e + tid.
+  const bool vec = (reinterpret_cast<uintptr_t>(z) & (4 * sizeof(T) - 1)) == 0 && (reinterpret_cast<uintptr_t>(out) & 15) == 0;
+  const int turns = kN ? kN : (n + 4 * kProbThreads - 1) / (4 * kProbThreads);
+  auto at = [&](int j, int e) { return j * 4 * kProbThreads + (vec ? tid * 4 + e : e * kProbThreads + tid); };
+  float x[kN ? kN : 1][4];
+  auto load = [&](int j, float (&y)[4]) {
+    if (vec && at(j, 3) < n) {
+      const float4 w = four(z + at(j, 0));
+      y[0] = w.x, y[1] = w.y, y[2] = w.z, y[3] = w.w;
+    } else {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) y[e] = at(j, e) < n ? up(z[at(j, e)]) : -INFINITY;
+    }
+  };
+  // f(turn, its four values)
+  auto each = [&](auto &&f) {
+    if (kN) {
+#pragma unroll
+      for (int j = 0; j < kN; ++j) f(j, x[j]);
+    } else {
+      for (int j = 0; j < turns; ++j) {
+        load(j, x[0]);
+        f(j, x[0]);
+      }
+    }
+  };
+  if (kN) {
+#pragma unroll
+    for (int j = 0; j < kN; ++j) load(j, x[j]);
+  }
 
-  // ---- the slice's largest logit
+  // ---- the slice's largest logit (greedy: and where it is first, and a NaN)
   float m = -INFINITY;
   int first = vocab, bad = !(t >= 0.f && t < INFINITY);
-  auto see = [&](float x, int i) {
-    if (x > m) {
-      m = x;
-      first = v0 + i;  // a thread meets its values in ascending order
-    }
-    bad |= x != x;
-    if (kept) e_s[i] = x;
-  };
-  int i0 = 0;
-  if (vec) {
-    i0 = n / kV * kV;
-#pragma unroll 4
-    for (int i = tid * kV; i < i0; i += kProbThreads * kV) {
-      const Vec16<T> w = *reinterpret_cast<const Vec16<T> *>(z + i);
+  each([&](int, const float (&y)[4]) { m = fmaxf(m, fmaxf(fmaxf(y[0], y[1]), fmaxf(y[2], y[3]))); });
+  if (greedy)
+    each([&](int j, const float (&y)[4]) {
 #pragma unroll
-      for (int k = 0; k < kV; ++k) see(up(w.x[k]), i + k);
-    }
-  }
-#pragma unroll 4
-  for (int i = i0 + tid; i < n; i += kProbThreads) see(up(z[i]), i);
-  auto join = [&](float x, int f) {
-    if (x > m || (x == m && f < first)) {
-      m = x;
+      for (int e = 0; e < 4; ++e) {
+        if (y[e] == m && at(j, e) < n) first = min(first, v0 + at(j, e));
+        bad |= y[e] != y[e];
+      }
+    });
+  auto join = [&](float y, int f) {
+    if (y > m || (y == m && f < first)) {
+      m = y;
       first = f;
     }
   };
 #pragma unroll
   for (int o = 16; o; o >>= 1) join(__shfl_xor_sync(~0u, m, o), __shfl_xor_sync(~0u, first, o));
-  bad = __any_sync(~0u, bad);
-  if (lane == 0) warp_part[warp] = Part{m, 0.f, first, bad};
-  __syncthreads();
-  for (int w = 0; w < kProbThreads / 32; ++w) {
-    join(warp_part[w].m, warp_part[w].first);
-    bad |= warp_part[w].bad;
-  }
+  if (lane == 0) warp_part[warp] = Part{m, 0.f, first, 0};
+  bad = __syncthreads_or(bad);
+#pragma unroll
+  for (int w = 0; w < kProbThreads / 32; ++w) join(warp_part[w].m, warp_part[w].first);
 
-  // ---- sum of exp((z - m) / T), in powers of two; log2(e) / T as two
-  // numbers, so that its rounding does not grow with z - m
-  const double c64 = greedy || bad ? 0.0 : 1.4426950408889634 / (double)t;
-  const float c_hi = (float)c64, c_lo = (float)(c64 - (double)c_hi), base = m == -INFINITY ? 0.f : m;
-  auto ex = [&](float x) {
-    const float d = x - base;
-    float y;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(fmaf(d, c_hi, d == -INFINITY ? 0.f : d * c_lo)));
-    return y;
+  // ---- sum of exp((z - m) / T), in powers of two (32-bit: the logit's
+  // difference, log2(e) / T and their product are each rounded once)
+  const float c = greedy || bad ? 0.f : (float)(1.4426950408889634 / (double)t), base = m == -INFINITY ? 0.f : m;
+  auto ex = [&](float y) {
+    float r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"((y - base) * c));
+    return r;
   };
   float l = 0.f;
-  if (!greedy) {
-    auto add = [&](int i) {
-      const float y = ex(kept ? e_s[i] : up(z[i]));
-      if (kept) e_s[i] = y;
-      l += y;
-    };
-    for (int i = tid * kV; i < i0; i += kProbThreads * kV)
+  if (!greedy && !bad)
+    each([&](int, float (&y)[4]) {
 #pragma unroll
-      for (int k = 0; k < kV; ++k) add(i + k);
-    for (int i = i0 + tid; i < n; i += kProbThreads) add(i);
+      for (int e = 0; e < 4; ++e) y[e] = ex(y[e]);
+      l += (y[0] + y[1]) + (y[2] + y[3]);
+    });
 #pragma unroll
-    for (int o = 16; o; o >>= 1) l += __shfl_xor_sync(~0u, l, o);
-  }
-  __syncthreads();  // warp_part is read
+  for (int o = 16; o; o >>= 1) l += __shfl_xor_sync(~0u, l, o);
   if (lane == 0) warp_part[warp].l = l;
   __syncthreads();
   if (tid == 0) {
@@ -132,47 +151,44 @@ __global__ void __launch_bounds__(kProbThreads) probs_kernel(const T *logits, lo
   cl.barrier_arrive();  // the others' parts are read
   __syncthreads();
   float M = -INFINITY, L = 0.f;
-  int at = vocab;
+  int best = vocab;
   bad = 0;
   for (int r = 0; r < C; ++r) {
     if (warp_part[r].m > M) {
       M = warp_part[r].m;
-      at = warp_part[r].first;
+      best = warp_part[r].first;
     }
     bad |= warp_part[r].bad;
   }
   const float Mb = M == -INFINITY ? 0.f : M;
-  auto to_row = [&](float x) {  // exp((x - M) / T), for a slice's largest logit x
-    const float d = x - Mb;
-    return exp2f(fmaf(d, c_hi, d == -INFINITY ? 0.f : d * c_lo));
-  };
-  for (int r = 0; r < C; ++r) L += warp_part[r].l * to_row(warp_part[r].m);
-  const bool none = bad || !(M > -INFINITY && M < INFINITY);
+  auto to_row = [&](float y) { return exp2f((y - Mb) * c); };  // exp((y - M) / T), for a slice's largest logit y
+  if (!greedy)
+    for (int r = 0; r < C; ++r) L += warp_part[r].l * to_row(warp_part[r].m);
+  // (a NaN among the logits shows in the sum)
+  const bool none = bad || L != L || !(M > -INFINITY && M < INFINITY);
   const float scale = none || greedy ? 0.f : to_row(m) / L;
 
   // ---- probabilities
-  auto p_of = [&](int i) {
-    if (greedy || none) return !none && v0 + i == at ? 1.f : 0.f;
-    return (kept ? e_s[i] : ex(up(z[i]))) * scale;
-  };
-  const bool vec_out = vec && (reinterpret_cast<uintptr_t>(out) & 15) == 0;
-  if (vec_out) {
-    for (int i = tid * kV; i < i0; i += kProbThreads * kV)
+  each([&](int j, float (&y)[4]) {
 #pragma unroll
-      for (int k = 0; k < kV; k += 4)
-        *reinterpret_cast<float4 *>(out + i + k) = make_float4(p_of(i + k), p_of(i + k + 1), p_of(i + k + 2), p_of(i + k + 3));
-  } else {
-    for (int i = tid * kV; i < i0; i += kProbThreads * kV)
+    for (int e = 0; e < 4; ++e) {
+      if (greedy || none) y[e] = !none && v0 + at(j, e) == best ? 1.f : 0.f;
+      else y[e] = (kN ? y[e] : ex(y[e])) * scale;
+    }
+    if (vec && at(j, 3) < n) {
+      *reinterpret_cast<float4 *>(out + at(j, 0)) = make_float4(y[0], y[1], y[2], y[3]);
+    } else {
 #pragma unroll
-      for (int k = 0; k < kV; ++k) out[i + k] = p_of(i + k);
-  }
-  for (int i = i0 + tid; i < n; i += kProbThreads) out[i] = p_of(i);
+      for (int e = 0; e < 4; ++e)
+        if (at(j, e) < n) out[at(j, e)] = y[e];
+    }
+  });
   cl.barrier_wait();
 }
 
 // ---------------------------------------------------------------- verification
 
-constexpr int kVerThreads = 512;
+constexpr int kVerThreads = 256;
 constexpr int kSeg = 512;  // values that a warp sums at a time: 16 per lane, in four runs of 128
 constexpr int kVerCluster = 8;
 constexpr int kMaxDrafted = 64;
@@ -204,16 +220,26 @@ struct Weights {  // the values r that the new token is drawn by
   }
 };
 
+__device__ __forceinline__ double scan_up(double x) {  // inclusive sums over the lanes
+  const int lane = threadIdx.x & 31;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const double y = __shfl_up_sync(~0u, x, o);
+    if (lane >= o) x += y;
+  }
+  return x;
+}
+
 // A cluster per sequence.  The tokens that stand follow from single values;
 // the new token from one row of p (and q), whose 64-bit sums are taken per
-// segment of kSeg values, per block, and over the cluster, always in that
-// order: the token is then found in the block, the segment and the lane that
-// the running sum passes u * sum in.  Bound by the memory latency of those
+// segment of kSeg values, over a block's segments, and over the cluster, always
+// in one order: the token is then found in the block, the segment and the lane
+// that the running sum passes u * sum in.  Bound by the memory latency of those
 // steps for few sequences, by reading the rows for many.
-__global__ void __launch_bounds__(kVerThreads) verify_kernel(const mk_verify_args a) {
-  extern __shared__ double seg[];  // sums of this block's segments
+__global__ void __launch_bounds__(kVerThreads, 4) verify_kernel(const mk_verify_args a) {
+  extern __shared__ double seg[];  // sums of this block's segments, then running sums
   __shared__ double total;
-  __shared__ int stop;
+  __shared__ int stop, again;
   cg::cluster_group cl = cg::this_cluster();
   const int C = cl.num_blocks(), rank = cl.block_rank();
   const int b = blockIdx.x / C, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -259,8 +285,8 @@ __global__ void __launch_bounds__(kVerThreads) verify_kernel(const mk_verify_arg
   w.q = acc < n && draft ? draft + acc * a.draft_row_stride : nullptr;
   w.without = acc < n && !draft ? tokens[acc] : -1;
   w.vec = ((reinterpret_cast<uintptr_t>(w.p) | reinterpret_cast<uintptr_t>(w.q)) & 15) == 0;
-  double sum = 0.0, before = 0.0;
-  for (int pass = 0; pass < 2; ++pass) {
+  double sum = 0.0, before = 0.0;  // (warp 0)
+  for (int pass = 0;; ++pass) {
     for (int s = s0 + warp; s < s1; s += kVerThreads / 32) {
       double x = 0.0, r[4][4];
 #pragma unroll
@@ -272,60 +298,77 @@ __global__ void __launch_bounds__(kVerThreads) verify_kernel(const mk_verify_arg
       if (lane == 0) seg[s - s0] = x;
     }
     __syncthreads();
-    if (tid == 0) {
-      double x = 0.0;
-      for (int s = 0; s < s1 - s0; ++s) x += seg[s];
-      total = x;
+    if (warp == 0) {
+      double run = 0.0;
+      for (int s = 0; s < s1 - s0; s += 32) {
+        const double x = run + scan_up(s + lane < s1 - s0 ? seg[s + lane] : 0.0);
+        if (s + lane < s1 - s0) seg[s + lane] = x;
+        run = __shfl_sync(~0u, x, 31);
+      }
+      if (lane == 0) total = run;
     }
     cl.sync();
-    sum = before = 0.0;
-    for (int r = 0; r < C; ++r) {
-      if (r == rank) before = sum;
-      sum += *cl.map_shared_rank(&total, r);
+    if (warp == 0) {
+      const double x = lane < C ? *cl.map_shared_rank(&total, lane) : 0.0;
+      // one after the other, so that a block's end is the next one's beginning
+      sum = before = 0.0;
+      for (int r = 0; r < C; ++r) {
+        if (r == rank) before = sum;
+        sum += __shfl_sync(~0u, x, r);
+      }
+      if (lane == 0) again = pass == 0 && acc < n && !(sum > 0.0);
     }
-    cl.sync();
-    if (sum > 0.0 || acc == n) break;
-    w.q = nullptr;  // p does not exceed q anywhere: draw by p itself
+    cl.barrier_arrive();  // the others' totals are read
+    __syncthreads();
+    if (!again) break;  // (the same in every block)
+    w.q = nullptr;      // p does not exceed q anywhere: draw by p itself
     w.without = -1;
+    cl.barrier_wait();
   }
-  if (!(sum > 0.0)) {
-    if (rank == 0 && tid == 0) out[acc] = -1;
-    return;
-  }
-  float uu = u[T];
-  uu = uu > 0.f ? fminf(uu, 0.99999994f) : 0.f;
-  const double goal = (double)uu * sum;  // < sum
-  if (!(before <= goal && before + total > goal) || warp) return;
-  double run = 0.0;
-  int s = 0;
-  for (; s < s1 - s0 - 1 && !(before + (run + seg[s]) > goal); ++s) run += seg[s];
-  run += before;
-  int found = -1, last = -1;  // last: the last value above 0, where rounding lets the sum stop short
-  for (int k = 0; k < 4 && found < 0; ++k) {
-    double r[4];
-    const int i = (s0 + s) * kSeg + k * 128 + lane * 4;
-    w.four(i, V, r);
-    const double mine = (r[0] + r[1]) + (r[2] + r[3]);
-    double x = mine;
+  if (warp == 0) {
+    if (!(sum > 0.0)) {
+      if (rank == 0 && lane == 0) out[acc] = -1;
+    } else {
+      float uu = u[T];
+      uu = uu > 0.f ? fminf(uu, 0.99999994f) : 0.f;
+      const double goal = (double)uu * sum;  // < sum
+      const double mine_to = seg[max(0, s1 - s0 - 1)];
+      // this block's sums go from `before` to before + mine_to
+      if (s1 > s0 && before <= goal && (before + mine_to > goal)) {
+        int s = s1 - s0 - 1;  // the first segment that passes the goal
+        for (int x = 0; x < s1 - s0; x += 32) {
+          const unsigned hit = __ballot_sync(~0u, x + lane < s1 - s0 && before + seg[x + lane] > goal);
+          if (hit) {
+            s = x + __ffs(hit) - 1;
+            break;
+          }
+        }
+        double run = before + (s > 0 ? seg[s - 1] : 0.0), r[4][4];
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const double y = __shfl_up_sync(~0u, x, o);
-      if (lane >= o) x += y;
-    }
-    double at = run + (x - mine);
-    int hit = -1, pos = -1;
+        for (int k = 0; k < 4; ++k) w.four((s0 + s) * kSeg + k * 128 + lane * 4, V, r[k]);
+        int found = -1, last = -1;  // last: the last value above 0, where rounding lets the sum stop short
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      at += r[e];
-      if (r[e] > 0.0) pos = i + e;
-      if (hit < 0 && r[e] > 0.0 && at > goal) hit = i + e;
+        for (int k = 0; k < 4; ++k) {
+          const int i = (s0 + s) * kSeg + k * 128 + lane * 4;
+          const double mine = (r[k][0] + r[k][1]) + (r[k][2] + r[k][3]), x = scan_up(mine);
+          double at = run + (x - mine);
+          int hit = -1, pos = -1;
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            at += r[k][e];
+            if (r[k][e] > 0.0) pos = i + e;
+            if (hit < 0 && r[k][e] > 0.0 && at > goal) hit = i + e;
+          }
+          const unsigned any = __ballot_sync(~0u, hit >= 0), some = __ballot_sync(~0u, pos >= 0);
+          if (any && found < 0) found = __shfl_sync(~0u, hit, __ffs(any) - 1);
+          if (some) last = __shfl_sync(~0u, pos, 31 - __clz(some));
+          run += __shfl_sync(~0u, x, 31);
+        }
+        if (lane == 0) out[acc] = found >= 0 ? found : last;
+      }
     }
-    const unsigned any = __ballot_sync(~0u, hit >= 0), some = __ballot_sync(~0u, pos >= 0);
-    if (any) found = __shfl_sync(~0u, hit, __ffs(any) - 1);
-    if (some) last = __shfl_sync(~0u, pos, 31 - __clz(some));
-    run += __shfl_sync(~0u, x, 31);
   }
-  if (lane == 0) out[acc] = found >= 0 ? found : last;
+  cl.barrier_wait();
 }
 
 }  // namespace
@@ -337,17 +380,16 @@ namespace {
 template <class T>
 int launch_probs(const void *logits, int64_t ls, const float *temperature, float *probs, int64_t ps, int n, int vocab,
                  cudaStream_t st) {
+  // A cluster of 8 for a large vocabulary, so that few rows still use many SMs
+  // and a slice fits into registers (up to 64 values a thread).
   const int C = vocab >= 16384 ? 8 : 1;
-  int per = (vocab + C - 1) / C;
-  per = (per + 15) / 16 * 16;
-  const size_t bytes = (size_t)per * 4;
-  const int kept = bytes <= 200 * 1024;
-  const size_t smem = kept ? bytes : 0;
-  int rc = serve_code(cudaFuncSetAttribute((const void *)probs_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                           200 * 1024));
-  if (rc) return rc;
-  return serve_launch(probs_kernel<T>, dim3((unsigned)n * C), kProbThreads, smem, st, false, C, (const T *)logits,
-                      (long long)ls, temperature, probs, (long long)ps, vocab, per, kept);
+  const int per = ((vocab + C - 1) / C + 15) / 16 * 16;
+  const int turns = (per + 4 * kProbThreads - 1) / (4 * kProbThreads);
+  void (*fn)(const T *, long long, const float *, float *, long long, int, int) =
+      turns <= 2 ? probs_kernel<T, 2> : turns <= 4 ? probs_kernel<T, 4> : turns <= 8 ? probs_kernel<T, 8> :
+      turns <= 16 ? probs_kernel<T, 16> : probs_kernel<T, 0>;
+  return serve_launch(fn, dim3((unsigned)n * C), kProbThreads, 0, st, false, C, (const T *)logits, (long long)ls,
+                      temperature, probs, (long long)ps, vocab, per);
 }
 }  // namespace
 
@@ -373,7 +415,8 @@ extern "C" int mk_verify(const mk_verify_args *a, void *stream) {
   const int C = kVerCluster;
   const size_t smem = ((size_t)(a->vocab + kSeg - 1) / kSeg + C - 1) / C * sizeof(double);
   if (smem > 200 * 1024) return MK_ERR_UNSUPPORTED_SHAPE;
-  int rc = smem > 40 * 1024 ? serve_code(cudaFuncSetAttribute((const void *)verify_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem)) : MK_OK;
+  static std::atomic<uint64_t> allowed;
+  int rc = smem > 40 * 1024 ? serve_allow_smem(allowed, (const void *)verify_kernel, 200 * 1024) : MK_OK;
   if (rc) return rc;
   return serve_launch(verify_kernel, dim3((unsigned)a->batch * C), kVerThreads, smem, (cudaStream_t)stream, false, C, *a);
 }

@@ -5,6 +5,7 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <atomic>
 #include <type_traits>
 
 #include "../../include/mk_serve.h"
@@ -45,6 +46,36 @@ int serve_launch(void (*fn)(A...), dim3 grid, int threads, size_t smem, cudaStre
   cfg.attrs = at;
   cfg.numAttrs = (unsigned)n;
   return serve_code(cudaLaunchKernelEx(&cfg, fn, static_cast<std::remove_const_t<A>>(args)...));
+}
+
+// Streaming multiprocessors of the current device (asked for once per device:
+// the calls here are short enough for the question to show).
+inline int serve_sms(int *out) {
+  static std::atomic<int> known[64];
+  int d = 0;
+  cudaError_t e = cudaGetDevice(&d);
+  if (e != cudaSuccess) return serve_code(e);
+  int n = d < 64 ? known[d].load(std::memory_order_relaxed) : 0;
+  if (n == 0) {
+    e = cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, d);
+    if (e != cudaSuccess) return serve_code(e);
+    if (d < 64) known[d].store(n, std::memory_order_relaxed);
+  }
+  *out = n;
+  return MK_OK;
+}
+// Allow fn `bytes` of dynamic shared memory on the current device (once per
+// device and function: `done` is the function's own).
+inline int serve_allow_smem(std::atomic<uint64_t> &done, const void *fn, size_t bytes) {
+  int d = 0;
+  cudaError_t e = cudaGetDevice(&d);
+  if (e != cudaSuccess) return serve_code(e);
+  const uint64_t bit = d < 64 ? 1ull << d : 0;
+  if (bit && (done.load(std::memory_order_relaxed) & bit)) return MK_OK;
+  e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+  if (e != cudaSuccess) return serve_code(e);
+  done.fetch_or(bit, std::memory_order_relaxed);
+  return MK_OK;
 }
 
 inline bool aligned_to(const void *p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }

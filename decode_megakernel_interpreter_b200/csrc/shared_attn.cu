@@ -1266,13 +1266,6 @@ void fill(const mk_attn_shared_args *a, AttnDev *d) {
   d->n_items = d->n_prefix_items + d->B * d->nkv * d->own_tiles;
 }
 
-int sm_count(int *out) {
-  int dev = 0;
-  cudaError_t e = cudaGetDevice(&dev);
-  if (e == cudaSuccess) e = cudaDeviceGetAttribute(out, cudaDevAttrMultiProcessorCount, dev);
-  return serve_code(e);
-}
-
 // The tensor map of K or V: boxes of 64 elements x `rows` positions of one head
 // of one page, with the 128-byte swizzle.
 bool make_map(CUtensorMap *map, const mk_attn_shared_args *a, const void *x, int rows) {
@@ -1313,7 +1306,8 @@ Sizes sizes_of(const AttnDev &d, int head_dim, int sms) {
 template <class T, int D>
 int launch(const AttnDev &p, const CUtensorMap (&maps)[2], int sms, cudaStream_t st) {
   static_assert(smem_stages<D>() + 4 * (kMaxRowsB + 1) + 1024 <= tc_smem<D>(), "the small items' stages and sums fit");
-  int rc = serve_code(cudaFuncSetAttribute((const void *)attn_kernel<T, D>, cudaFuncAttributeMaxDynamicSharedMemorySize, tc_smem<D>()));
+  static std::atomic<uint64_t> allowed;
+  int rc = serve_allow_smem(allowed, (const void *)attn_kernel<T, D>, tc_smem<D>());
   if (!rc) rc = serve_launch(attn_kernel<T, D>, dim3(sms), kTcThreads, tc_smem<D>(), st, false, 1, p, maps[0], maps[1]);
   if (rc) return rc;
   const dim3 grid((p.B * p.T * p.G + kJoinRows - 1) / kJoinRows, p.nkv);
@@ -1330,7 +1324,7 @@ extern "C" int64_t mk_attn_shared_workspace_bytes(const mk_attn_shared_args *a) 
   AttnDev d;
   fill(a, &d);
   int sms = 0;
-  if (sm_count(&sms)) return 0;
+  if (serve_sms(&sms)) return 0;
   const Sizes z = sizes_of(d, a->head_dim, sms);
   return z.part_o + z.part_ml + z.tc_o + z.tc_ml + z.who + z.tc_who + z.how;
 }
@@ -1379,7 +1373,7 @@ extern "C" int mk_attn_shared(const mk_attn_shared_args *a, void *workspace, voi
   d.scale2 = std::max(1e-37f, (float)(std::fabs((double)a->scale) * 1.4426950408889634));
   d.flip = a->scale < 0.f ? 0x80008000u : 0u;
   int sms = 0;
-  if ((rc = sm_count(&sms))) return rc;
+  if ((rc = serve_sms(&sms))) return rc;
   const Sizes z = sizes_of(d, a->head_dim, sms);
   char *w = (char *)workspace;
   auto part = [&](int64_t bytes) {  // the sizes are multiples of 16, but for the last ones' of 8 and 4

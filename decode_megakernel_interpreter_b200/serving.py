@@ -28,13 +28,17 @@ def _need(ok, what: str) -> None:
 
 def _ints(t, n: int, name: str, dev) -> int:
     """The address of a contiguous int32 tensor of at least n words on `dev`."""
-    _need(t.dtype is torch.int32 and t.is_contiguous() and t.numel() >= n and t.device == dev,
-          f"{name}: a contiguous int32 tensor of at least {n} words on {dev}")
+    if not (t.dtype is torch.int32 and t.is_contiguous() and t.numel() >= n and t.device == dev):
+        raise ValueError(f"{name}: a contiguous int32 tensor of at least {n} words on {dev}")
     return t.data_ptr()
 
 
 def _status(t, dev):
     return None if t is None else _ints(t, 1, "status", dev)
+
+
+def _current_device() -> int:
+    return torch.cuda.current_device()
 
 
 class _On:
@@ -43,14 +47,15 @@ class _On:
     __slots__ = ("raw", "ctx")
 
     def __init__(self, dev, stream):
-        _need(dev.type == "cuda", "tensors must be CUDA tensors")
+        if dev.type != "cuda":
+            raise ValueError("tensors must be CUDA tensors")
         self.ctx = None
         if stream is not None:
             _need(stream.device == dev, "the stream is another device's")
             self.ctx = torch.cuda.stream(stream)
             self.raw = stream.cuda_stream
         else:
-            if dev.index != torch.cuda.current_device():
+            if dev.index != _current_device():
                 self.ctx = torch.cuda.device(dev)
             self.raw = torch._C._cuda_getCurrentRawStream(dev.index)
 
@@ -201,17 +206,22 @@ def shared_attention(q, k, v, table, lens, prefix_pages=None, prefix_len=None, s
     a pool, [pages][kv heads][page][head_dim]; table: int32 [batch][pages of a sequence]; lens: int32 [batch], prefix
     included (negative: the sequence is unused and its output rows stay as they are); prefix_pages: int32 pages of the
     prefix; prefix_len: int32, one word.  Returns out like q, or (out, lse) with lse float [batch][tokens][q heads]."""
-    _need(q.dim() == 4 and k.dim() == 4 and k.shape == v.shape and k.stride() == v.stride(),
-          "q: [batch][tokens][heads][head_dim]; k and v: [pages][kv heads][page][head_dim] of one shape and strides")
+    if q.dim() != 4 or k.dim() != 4 or k.shape != v.shape or k.stride() != v.stride():
+        raise ValueError("q: [batch][tokens][heads][head_dim]; k and v: [pages][kv heads][page][head_dim] of one shape "
+                         "and strides")
     B, T, nq, d = q.shape
     n_pages, nkv, page, dk = k.shape
-    dev = q.device
-    _need(d == dk and q.dtype in DTYPES and q.dtype is k.dtype and q.dtype is v.dtype and k.device == dev and
-          v.device == dev, "q, k and v agree in head_dim, type and device")
-    _need(q.stride(3) == 1 and k.stride(3) == 1, "the last dimension must be contiguous")
-    _need(table.dim() == 2 and table.shape[0] == B, "table: [batch][pages]")
+    dev, dtype = q.device, q.dtype
+    qs, ks = q.stride(), k.stride()
+    code = DTYPES.get(dtype)
+    if d != dk or code is None or dtype is not k.dtype or dtype is not v.dtype or k.device != dev or v.device != dev:
+        raise ValueError("q, k and v agree in head_dim, type and device")
+    if qs[3] != 1 or ks[3] != 1:
+        raise ValueError("the last dimension must be contiguous")
+    if table.dim() != 2 or table.shape[0] != B:
+        raise ValueError("table: [batch][pages]")
     if out is not None:
-        _need(out.shape == q.shape and out.dtype is q.dtype and out.device == dev and out.stride(3) == 1,
+        _need(out.shape == q.shape and out.dtype is dtype and out.device == dev and out.stride(3) == 1,
               "out: like q, its last dimension contiguous")
     if lse is not None:
         _need(lse.shape == (B, T, nq) and lse.dtype is torch.float32 and lse.is_contiguous() and lse.device == dev,
@@ -224,19 +234,19 @@ def shared_attention(q, k, v, table, lens, prefix_pages=None, prefix_len=None, s
         pp = pl = None
     with _On(dev, stream) as s:
         if out is None:
-            out = torch.empty((B, T, nq, d), dtype=q.dtype, device=dev)
+            out = q.new_empty((B, T, nq, d))
         if lse is None and return_lse:
-            lse = torch.empty((B, T, nq), dtype=torch.float32, device=dev)
-        qs, os, ks = q.stride(), out.stride(), k.stride()
+            lse = q.new_empty((B, T, nq), dtype=torch.float32)
+        os = out.stride()
         a = mk_attn_shared_args(
-            B, T, nq, nkv, d, DTYPES[q.dtype], page, n_pages, n_prefix, table.shape[1],
+            B, T, nq, nkv, d, code, page, n_pages, n_prefix, table.shape[1],
             1.0 / math.sqrt(d) if scale is None else scale, q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(),
             lse.data_ptr() if lse is not None else None, pp, pl, _ints(table, 1, "table", dev),
             _ints(lens, B, "lens", dev), _status(status, dev), qs[0], qs[1], qs[2], os[0], os[1], os[2],
             ks[0], ks[1], ks[2])
         L, ref = load(), ctypes.byref(a)
         n = L.mk_attn_shared_workspace_bytes(ref)
-        ws = torch.empty(max(n, 256), dtype=torch.uint8, device=dev)
+        ws = table.new_empty(max(n, 256) // 4 + 1)
         _check(L.mk_attn_shared(ref, ws.data_ptr(), s), "mk_attn_shared")
     return (out, lse) if return_lse else out
 

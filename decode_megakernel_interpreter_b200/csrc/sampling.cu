@@ -54,7 +54,7 @@ __device__ __forceinline__ float4 four(const T *z) {  // 16-bit types
 // memory; a vocabulary too large for that (kN = 0) is read three times.  Bound
 // by memory: each logit read and each probability written once.
 template <class T, int kN>
-__global__ void __launch_bounds__(kProbThreads) probs_kernel(const T *logits, long long ls, const float *temperature,
+__global__ void __launch_bounds__(kProbThreads, kN <= 8 ? 2 : 1) probs_kernel(const T *logits, long long ls, const float *temperature,
                                                              float *probs, long long ps, int vocab, int per) {
   __shared__ Part part, warp_part[kProbThreads / 32];
   cg::cluster_group cl = cg::this_cluster();
@@ -183,6 +183,131 @@ __global__ void __launch_bounds__(kProbThreads) probs_kernel(const T *logits, lo
         if (at(j, e) < n) out[at(j, e)] = y[e];
     }
   });
+  cl.barrier_wait();
+}
+
+// The same for many rows, where registers would hold too few of them at a time:
+// a block reads its slice twice, first for the maximum and the sum, then, out
+// of L2, for the probabilities.  The slices of all blocks on the chip are about
+// 60 MB, so DRAM still sees each logit once.  (512 rows of 128256 on a B200:
+// 174 us in registers.)
+constexpr int kStreamThreads = 512;
+constexpr int kStreamTurns = 4;  // fours that a thread loads at a time
+template <class T>
+__global__ void __launch_bounds__(kStreamThreads, 3) probs_stream_kernel(const T *logits, long long ls, const float *temperature,
+                                                                         float *probs, long long ps, int vocab, int per) {
+  __shared__ Part part, warp_part[kStreamThreads / 32];
+  cg::cluster_group cl = cg::this_cluster();
+  const int C = cl.num_blocks(), rank = cl.block_rank();
+  const int row = blockIdx.x / C, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int v0 = min(rank * per, vocab), n = min(per, vocab - v0);
+  const T *z = logits + row * ls + v0;
+  float *out = probs + row * ps + v0;
+  const float t = temperature ? temperature[row] : 1.f;
+  const bool greedy = t == 0.f;
+  const int bad_t = !(t >= 0.f && t < INFINITY);
+  const float c = greedy || bad_t ? 0.f : (float)(1.4426950408889634 / (double)t);
+  const bool vec = (reinterpret_cast<uintptr_t>(z) & (4 * sizeof(T) - 1)) == 0 && (reinterpret_cast<uintptr_t>(out) & 15) == 0;
+  auto at = [&](int j, int e) { return j * 4 * kStreamThreads + (vec ? tid * 4 + e : e * kStreamThreads + tid); };
+  const int turns = (n + 4 * kStreamThreads - 1) / (4 * kStreamThreads);
+  auto load = [&](int j0, float (&y)[kStreamTurns][4]) {
+#pragma unroll
+    for (int j = 0; j < kStreamTurns; ++j)
+      if (vec && at(j0 + j, 3) < n) {
+        const float4 w = four(z + at(j0 + j, 0));
+        y[j][0] = w.x, y[j][1] = w.y, y[j][2] = w.z, y[j][3] = w.w;
+      } else {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) y[j][e] = at(j0 + j, e) < n ? up(z[at(j0 + j, e)]) : -INFINITY;
+      }
+  };
+  auto ex = [&](float y, float base) {
+    float r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"((y - base) * c));
+    return r;
+  };
+  float m = -INFINITY, l = 0.f, y[kStreamTurns][4];
+  int first = vocab, bad = bad_t;
+  for (int j0 = 0; j0 < turns; j0 += kStreamTurns) {
+    load(j0, y);
+    float top = -INFINITY;
+#pragma unroll
+    for (int j = 0; j < kStreamTurns; ++j) top = fmaxf(top, fmaxf(fmaxf(y[j][0], y[j][1]), fmaxf(y[j][2], y[j][3])));
+    if (greedy) {
+#pragma unroll
+      for (int j = 0; j < kStreamTurns; ++j)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          bad |= y[j][e] != y[j][e];
+          // (a thread meets its values in ascending order when they come by fours; else by turns)
+          if (at(j0 + j, e) < n && (y[j][e] > m || (y[j][e] == m && v0 + at(j0 + j, e) < first))) {
+            m = y[j][e];
+            first = v0 + at(j0 + j, e);
+          }
+        }
+    } else {
+      if (top > m) {
+        l *= m == -INFINITY ? 0.f : ex(m, top);
+        m = top;
+      }
+      const float base = m == -INFINITY ? 0.f : m;
+#pragma unroll
+      for (int j = 0; j < kStreamTurns; ++j) l += (ex(y[j][0], base) + ex(y[j][1], base)) + (ex(y[j][2], base) + ex(y[j][3], base));
+    }
+  }
+  auto join = [&](float m2, float l2, int f2) {
+    if (greedy) {
+      if (m2 > m || (m2 == m && f2 < first)) {
+        m = m2;
+        first = f2;
+      }
+      return;
+    }
+    const float top = fmaxf(m, m2), base = top == -INFINITY ? 0.f : top;
+    l = l * ex(m, base) + l2 * ex(m2, base);
+    m = top;
+  };
+#pragma unroll
+  for (int o = 16; o; o >>= 1) join(__shfl_xor_sync(~0u, m, o), __shfl_xor_sync(~0u, l, o), __shfl_xor_sync(~0u, first, o));
+  if (lane == 0) warp_part[warp] = Part{m, l, first, 0};
+  bad = __syncthreads_or(bad);
+  if (warp == 0) {
+    const Part q = lane < kStreamThreads / 32 ? warp_part[lane] : Part{-INFINITY, 0.f, vocab, 0};
+    m = q.m;
+    l = q.l;
+    first = q.first;
+#pragma unroll
+    for (int o = 16; o; o >>= 1) join(__shfl_xor_sync(~0u, m, o), __shfl_xor_sync(~0u, l, o), __shfl_xor_sync(~0u, first, o));
+    if (lane == 0) part = Part{m, l, first, bad};
+  }
+  cl.sync();
+  if (tid < C) warp_part[tid] = *cl.map_shared_rank(&part, tid);
+  cl.barrier_arrive();  // the others' parts are read
+  __syncthreads();
+  m = -INFINITY, l = 0.f, first = vocab;
+  bad = 0;
+  for (int r = 0; r < C; ++r) {
+    join(warp_part[r].m, warp_part[r].l, warp_part[r].first);
+    bad |= warp_part[r].bad;
+  }
+  const bool none = bad || l != l || !(m > -INFINITY && m < INFINITY);
+  const float scale = none || greedy ? 0.f : 1.f / l, base = none ? 0.f : m;
+  for (int j0 = 0; j0 < turns; j0 += kStreamTurns) {
+    if (!greedy && !none) load(j0, y);
+#pragma unroll
+    for (int j = 0; j < kStreamTurns; ++j) {
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        y[j][e] = greedy || none ? (!none && v0 + at(j0 + j, e) == first ? 1.f : 0.f) : ex(y[j][e], base) * scale;
+      if (vec && at(j0 + j, 3) < n) {
+        __stcs(reinterpret_cast<float4 *>(out + at(j0 + j, 0)), make_float4(y[j][0], y[j][1], y[j][2], y[j][3]));
+      } else {
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          if (at(j0 + j, e) < n) out[at(j0 + j, e)] = y[j][e];
+      }
+    }
+  }
   cl.barrier_wait();
 }
 
@@ -388,6 +513,13 @@ int launch_probs(const void *logits, int64_t ls, const float *temperature, float
   void (*fn)(const T *, long long, const float *, float *, long long, int, int) =
       turns <= 2 ? probs_kernel<T, 2> : turns <= 4 ? probs_kernel<T, 4> : turns <= 8 ? probs_kernel<T, 8> :
       turns <= 16 ? probs_kernel<T, 16> : probs_kernel<T, 0>;
+  int sms = 0, rc = serve_sms(&sms);
+  if (rc) return rc;
+  if (vocab >= 16384 && (long long)n * C > 2 * sms) {
+    const int few = 4, slice = ((vocab + few - 1) / few + 15) / 16 * 16;
+    return serve_launch(probs_stream_kernel<T>, dim3((unsigned)n * few), kStreamThreads, 0, st, false, few, (const T *)logits,
+                        (long long)ls, temperature, probs, (long long)ps, vocab, slice);
+  }
   return serve_launch(fn, dim3((unsigned)n * C), kProbThreads, 0, st, false, C, (const T *)logits, (long long)ls,
                       temperature, probs, (long long)ps, vocab, per);
 }

@@ -322,8 +322,10 @@ struct Weights {  // the values r that the new token is drawn by
   const float *p, *q;
   int without;    // a token of weight 0 (-1: none)
   bool vec;       // both rows are 16-byte aligned
-  __device__ __forceinline__ static double pos(float x) { return x > 0.f && x < INFINITY ? (double)x : 0.0; }
-  // 4 values from i on, i a multiple of 4 (0 from n on)
+  // x, or 0 where it is not above 0 or not finite
+  __device__ __forceinline__ static float pos(float x) { return x < INFINITY ? fmaxf(x, 0.f) : 0.f; }
+  // 4 values from i on, i a multiple of 4 (0 from n on).  max(p - q, 0) as
+  // p - min(q, p): the comparison in 32 bits, the exact difference in 64.
   __device__ __forceinline__ void four(int i, int n, double (&r)[4]) const {
     float a[4], b[4] = {0.f, 0.f, 0.f, 0.f};
     if (vec && i + 4 <= n) {
@@ -340,8 +342,16 @@ struct Weights {  // the values r that the new token is drawn by
         if (q) b[k] = i + k < n ? __ldg(q + i + k) : 0.f;
       }
     }
+    if (without >= i && without < i + 4) {
 #pragma unroll
-    for (int k = 0; k < 4; ++k) r[k] = i + k == without ? 0.0 : fmax(pos(a[k]) - pos(b[k]), 0.0);
+      for (int k = 0; k < 4; ++k)
+        if (i + k == without) a[k] = 0.f;
+    }
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      a[k] = pos(a[k]);
+      r[k] = q ? (double)a[k] - (double)fminf(pos(b[k]), a[k]) : (double)a[k];
+    }
   }
 };
 
@@ -386,8 +396,8 @@ __global__ void __launch_bounds__(kVerThreads, 4) verify_kernel(const mk_verify_
     const int x = tokens[tid];
     bool ok = (unsigned)x < (unsigned)V;
     if (ok) {
-      const double px = Weights::pos(target[tid * a.target_row_stride + x]);
-      const double qx = draft ? Weights::pos(draft[tid * a.draft_row_stride + x]) : 1.0;
+      const double px = (double)Weights::pos(target[tid * a.target_row_stride + x]);
+      const double qx = draft ? (double)Weights::pos(draft[tid * a.draft_row_stride + x]) : 1.0;
       ok = (double)u[tid] * qx < px;
     } else {
       report(a.status, MK_ERR_DEVICE_INPUT);

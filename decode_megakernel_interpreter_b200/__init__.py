@@ -203,6 +203,10 @@ def load(path: str = LIB_PATH):
     L.mk_attn_shared.argtypes = [P(mk_attn_shared_args), vp, vp]
     L.mk_token_probs.restype = i32
     L.mk_token_probs.argtypes = [vp, i32, i64, vp, vp, i64, i32, i32, vp]
+    L.mk_speculate.restype = i32
+    L.mk_speculate.argtypes = [vp, i32, vp, i32, i32, vp, vp, vp, vp, vp, vp]
+    L.mk_decode_step_shared.restype = i32
+    L.mk_decode_step_shared.argtypes = [vp, vp, vp, i32, i32, vp, vp, vp]
     L.mk_verify.restype = i32
     L.mk_verify.argtypes = [P(mk_verify_args), vp]
     _lib = L
@@ -411,6 +415,52 @@ class Engine:
                         _ptr(logits_out) if logits_out is not None else None, _ptr(next_token_out), s.cuda_stream)
         if rc != MK_OK:
             raise MkError(rc, "mk_prefill")
+
+    def decode_step_shared(self, tokens, positions, prefix_seq, prefix_len, logits_out, next_tokens_out,
+                           stream=None) -> None:
+        """decode_step of a plan with exec_mode="per_op" whose sequences share the first prefix_len positions, read
+        once from sequence prefix_seq's rows of the cache."""
+        import torch
+        s = stream if stream is not None else torch.cuda.current_stream()
+        rc = load().mk_decode_step_shared(self.h, _ptr(tokens), _ptr(positions), prefix_seq, prefix_len,
+                                          _ptr(logits_out) if logits_out is not None else None,
+                                          _ptr(next_tokens_out), s.cuda_stream)
+        if rc != MK_OK:
+            raise MkError(rc, "mk_decode_step_shared")
+
+    def speculate(self, seq, tokens, pos0, u, out_tokens, n_accepted, draft_probs=None, temperature=None,
+                  stream=None) -> None:
+        """Check drafted tokens: `tokens` (device int32) is sequence `seq`'s last token, at pos0, and the drafted ones
+        after it; the tokens that stand and the one sampled after them go to out_tokens, their count to n_accepted."""
+        import torch
+        s = stream if stream is not None else torch.cuda.current_stream()
+        n = int(tokens.numel())
+        for t, k, dtype in ((tokens, n, torch.int32), (u, n, torch.float32), (out_tokens, n, torch.int32),
+                            (n_accepted, 1, torch.int32), (draft_probs, (n - 1) * self.cfg.vocab, torch.float32),
+                            (temperature, 1, torch.float32)):
+            if t is not None and (t.dtype is not dtype or t.numel() < k):
+                raise ValueError(f"speculate: a {dtype} tensor of at least {k} elements is needed")
+        rc = load().mk_speculate(self.h, seq, _ptr(tokens), n, pos0, _ptr(draft_probs), _ptr(temperature), _ptr(u),
+                                 _ptr(out_tokens), _ptr(n_accepted), s.cuda_stream)
+        if rc != MK_OK:
+            raise MkError(rc, "mk_speculate")
+
+    def fork(self, seq: int, children, n_rows: int, stream=None) -> None:
+        """Copy the first n_rows K/V rows of sequence `seq` to the sequences `children` (a prompt prefilled once and
+        continued several times)."""
+        import torch
+        from .serving import KvPool, kv_copy
+        kc, vc = self._keep[1], self._keep[2]
+        kids = [int(c) for c in children]
+        if (not kids or len(set(kids)) != len(kids) or seq in kids or not 0 <= n_rows <= self.cfg.max_seq or
+                not all(0 <= c < self.cfg.max_batch for c in kids + [seq])):
+            raise ValueError("fork: children are other sequences, each once; n_rows at most max_seq")
+        shape = (self.cfg.n_layers, self.cfg.max_batch, self.cfg.n_kv_heads, self.cfg.max_seq, self.cfg.head_dim)
+        pool = KvPool(kc.view(shape), vc.view(shape))
+        items = torch.tensor([[seq, 0, c, 0, n_rows] for c in kids], dtype=torch.int32, device=kc.device)
+        if stream is not None:
+            items.record_stream(stream)
+        kv_copy(pool, pool, items, stream=stream)
 
     def status(self, stream=None) -> int:
         import torch

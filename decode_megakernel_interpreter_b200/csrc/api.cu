@@ -16,6 +16,7 @@
 #include "interp_launch.h"
 #include "mk_internal.h"
 #include "planner.h"
+#include "serve_common.h"
 
 using namespace mk;
 
@@ -56,6 +57,15 @@ struct mk_handle {
   // (allocated with the plan on first use)
   float *pf_logits = nullptr;
   int *pf_next = nullptr;
+  // mk_speculate's scratch: logits and probabilities of kMaxBatch rows, their
+  // greedy tokens (allocated with the plan on first use)
+  float *sp_logits = nullptr, *sp_probs = nullptr;
+  int *sp_next = nullptr;
+  // mk_decode_step_shared's scratch: the page list and lengths of the attention
+  // call, its workspace
+  int *sh_words = nullptr;  // [0] prefix page, [1] prefix length, then lens[B], table[B]
+  void *sh_ws = nullptr;
+  bool sh_skipped = false;  // the attention instructions did not run in the last step
   int last_detail[6] = {0, 0, 0, 0, 0, 0};
   // per-op graph mode
   cudaGraphExec_t gexec = nullptr;
@@ -482,6 +492,11 @@ static void drop_plan(mk_handle *h) {
   free_list(h->plan_allocs);
   h->pf_logits = nullptr;
   h->pf_next = nullptr;
+  h->sp_logits = h->sp_probs = nullptr;
+  h->sp_next = nullptr;
+  h->sh_words = nullptr;
+  h->sh_ws = nullptr;
+  h->sh_skipped = false;
   h->planned = false;
 }
 
@@ -755,9 +770,80 @@ extern "C" int mk_plan(mk_handle *h, const mk_plan_opts *opts_in) {
   return MK_OK;
 }
 
-static int launch_per_op(mk_handle *h, KParams k, cudaStream_t st) {
+// What a step whose attention instructions did not run left behind: a merge
+// ticket behind the step number, and tagged partials that are older than the one
+// step which their 2-bit tags tell apart.  Both as the last step would have left
+// them.
+static __global__ void resync_attn_kernel(KParams k) {
+  const unsigned epoch = *k.epoch;
+  const long long n = (long long)k.L * k.B * k.nq * k.S * k.d, i0 = blockIdx.x * (long long)blockDim.x + threadIdx.x;
+  for (long long i = i0; i < n; i += (long long)gridDim.x * blockDim.x)
+    reinterpret_cast<unsigned *>(k.part_o)[i] = (epoch - 1u) & 3u;
+  const int tickets = k.L * k.B * k.nkv;
+  for (int i = (int)i0; i < tickets; i += (int)(gridDim.x * blockDim.x)) k.ctr[k.attn_ticket0 + i] = (epoch - 1u) * (unsigned)k.S;
+}
+// The words of a shared step's attention calls.
+static __global__ void shared_words_kernel(int *words, const int *positions, int B, int max_seq, int prefix_seq, int prefix_len,
+                                           int *status) {
+  const int b = threadIdx.x;
+  if (b == 0) {
+    words[0] = prefix_seq;
+    words[1] = prefix_len;
+  }
+  if (b < B) {
+    const int pos = min(max(positions[b], 0), max_seq - 1);
+    if (pos < prefix_len) atomicCAS(status, 0, MK_ERR_DEVICE_INPUT);
+    words[2 + b] = pos + 1;
+    words[2 + B + b] = b;
+  }
+}
+// The attention stage of layer l in a shared step.
+static int shared_attention(mk_handle *h, const KParams &k, int l, cudaStream_t st) {
+  const size_t n = (size_t)k.B * k.qdim;
+  mk_attn_shared_args a;
+  memset(&a, 0, sizeof a);
+  a.batch = k.B;
+  a.n_tokens = 1;
+  a.n_q_heads = k.nq;
+  a.n_kv_heads = k.nkv;
+  a.head_dim = k.d;
+  a.dtype = MK_DTYPE_BF16;
+  a.page = k.max_seq;
+  a.n_pages = h->cfg.max_batch;
+  a.n_prefix_pages = 1;
+  a.table_width = 1;
+  a.scale = k.attn_scale;
+  a.q = k.qbuf + l * n;
+  a.k = k.kc + (size_t)l * k.kv_ls;
+  a.v = k.vc + (size_t)l * k.kv_ls;
+  a.out = k.obuf + l * n;
+  a.prefix_pages = h->sh_words;
+  a.prefix_len = h->sh_words + 1;
+  a.lens = h->sh_words + 2;
+  a.table = h->sh_words + 2 + k.B;
+  a.status = k.status;
+  a.q_batch_stride = a.q_token_stride = a.out_batch_stride = a.out_token_stride = k.qdim;
+  a.q_head_stride = a.out_head_stride = a.row_stride = k.d;
+  a.page_stride = k.kv_bs;
+  a.kv_head_stride = k.kv_hs;
+  return attn_shared_tagged(&a, k.obuf + l * n, k.epoch, h->sh_ws, st);
+}
+
+static int launch_per_op(mk_handle *h, KParams k, cudaStream_t st, bool shared = false) {
+  if (!shared && h->sh_skipped) {
+    resync_attn_kernel<<<4 * h->sm_count, 256, 0, st>>>(k);
+    cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess) return cuda_code(e);
+    h->sh_skipped = false;
+  }
   const int n_stage = h->shape.L * kStagesPerLayer + 1;
   for (int sidx = 0; sidx < n_stage; ++sidx) {
+    if (shared && sidx < n_stage - 1 && sidx % kStagesPerLayer == ST_ATTN) {
+      h->sh_skipped = true;
+      const int rc = shared_attention(h, k, sidx / kStagesPerLayer, st);
+      if (rc) return rc;
+      continue;
+    }
     // skip the empty per-layer stage slot of the LM head
     k.stage_filter = sidx;
     k.mode = (h->kp.mode & MODE_TRACE) | MODE_NO_WAIT | (sidx == n_stage - 1 ? MODE_FINAL_LAUNCH : 0u);
@@ -768,6 +854,43 @@ static int launch_per_op(mk_handle *h, KParams k, cudaStream_t st) {
     }
   }
   return MK_OK;
+}
+
+extern "C" int mk_decode_step_shared(mk_handle *h, const int32_t *tokens, const int32_t *positions, int32_t prefix_seq,
+                                     int32_t prefix_len, float *logits_out, int32_t *next_tokens_out, void *stream) {
+  if (!h || !tokens || !positions || !next_tokens_out) return MK_ERR_INVALID_ARG;
+  if (!h->planned) return MK_ERR_NOT_PLANNED;
+  if (h->opts.exec_mode != MK_EXEC_PER_OP || prefix_seq < 0 || prefix_seq >= h->cfg.max_batch || prefix_len < 0 ||
+      prefix_len > h->cfg.max_seq)
+    return MK_ERR_INVALID_ARG;
+  cudaStream_t st = (cudaStream_t)stream;
+  KParams k = h->kp;
+  if (!h->sh_ws) {
+    int rc;
+    mk_attn_shared_args a;
+    memset(&a, 0, sizeof a);
+    a.batch = k.B;
+    a.n_tokens = a.n_prefix_pages = a.table_width = 1;
+    a.n_q_heads = k.nq;
+    a.n_kv_heads = k.nkv;
+    a.head_dim = k.d;
+    a.page = k.max_seq;
+    a.n_pages = h->cfg.max_batch;
+    const int64_t bytes = mk_attn_shared_workspace_bytes(&a);
+    if (bytes <= 0) return MK_ERR_UNSUPPORTED_SHAPE;
+    char *ws = nullptr;
+    if ((rc = dalloc(h->plan_allocs, &h->sh_words, 2 + 2 * (size_t)k.B, false))) return rc;
+    if ((rc = dalloc(h->plan_allocs, &ws, (size_t)bytes, false))) return rc;
+    h->sh_ws = ws;
+  }
+  k.tokens = tokens;
+  k.positions = positions;
+  k.logits = logits_out;
+  k.next_tokens = next_tokens_out;
+  shared_words_kernel<<<1, 32, 0, st>>>(h->sh_words, positions, k.B, k.max_seq, prefix_seq, prefix_len, k.status);
+  cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess) return cuda_code(e);
+  return launch_per_op(h, k, st, true);
 }
 
 extern "C" int mk_decode_step(mk_handle *h, const int32_t *tokens, const int32_t *positions, float *logits_out,
@@ -863,6 +986,57 @@ extern "C" int mk_prefill(mk_handle *h, int32_t seq, const int32_t *tokens, int3
                             cudaMemcpyDeviceToDevice, st));
   MK_CUDA(cudaMemcpyAsync(next_token_out, h->pf_next + (last_n - 1), sizeof(int32_t), cudaMemcpyDeviceToDevice, st));
   return MK_OK;
+}
+
+extern "C" int mk_speculate(mk_handle *h, int32_t seq, const int32_t *tokens, int32_t n_tokens, int32_t pos0,
+                            const float *draft_probs, const float *temperature, const float *u, int32_t *out_tokens,
+                            int32_t *n_accepted, void *stream) {
+  if (!h || !tokens || !u || !out_tokens || !n_accepted || n_tokens < 1 || n_tokens > kMaxBatch || pos0 < 0)
+    return MK_ERR_INVALID_ARG;
+  if (!h->planned) return MK_ERR_NOT_PLANNED;
+  if (seq < 0 || seq >= h->cfg.max_batch || (int64_t)pos0 + n_tokens > h->cfg.max_seq) return MK_ERR_INVALID_ARG;
+  if (h->opts.exec_mode != MK_EXEC_MEGAKERNEL && h->opts.exec_mode != MK_EXEC_MEGAKERNEL_GENERIC)
+    return MK_ERR_INVALID_ARG;
+  cudaStream_t st = (cudaStream_t)stream;
+  const int B = h->kp.B, V = h->kp.V;
+  int rc;
+  if (!h->sp_next) {
+    if ((rc = dalloc(h->plan_allocs, &h->sp_logits, (size_t)kMaxBatch * V, false))) return rc;
+    if ((rc = dalloc(h->plan_allocs, &h->sp_probs, (size_t)kMaxBatch * V, false))) return rc;
+    if ((rc = dalloc(h->plan_allocs, &h->sp_next, (size_t)kMaxBatch, false))) return rc;
+  }
+  // chunks of up to B tokens a launch, as mk_prefill, each row's logits kept
+  for (int c0 = 0; c0 < n_tokens; c0 += B) {
+    KParams k = h->kp;
+    k.chunk_n = std::min(B, n_tokens - c0);
+    k.chunk_pos0 = pos0 + c0;
+    k.kv_seq0 = seq;
+    k.tokens = tokens + c0;
+    k.positions = tokens + c0;  // unused for chunks
+    k.logits = h->sp_logits + (size_t)c0 * V;
+    k.next_tokens = h->sp_next;
+    k.mode |= MODE_FINAL_LAUNCH;
+    cudaError_t e = launch_interp(h->kernel, k, h->grid, h->smem, st, true);
+    if (e != cudaSuccess) {
+      cudaGetLastError();
+      return cuda_code(e);
+    }
+  }
+  if ((rc = token_probs(h->sp_logits, MK_DTYPE_F32, V, temperature, 0, h->sp_probs, V, n_tokens, V, stream))) return rc;
+  mk_verify_args a;
+  memset(&a, 0, sizeof a);
+  a.batch = 1;
+  a.max_drafted = n_tokens - 1;
+  a.vocab = V;
+  a.target = h->sp_probs;
+  a.draft = draft_probs;
+  a.tokens = tokens + 1;
+  a.u = u;
+  a.out_tokens = out_tokens;
+  a.n_accepted = n_accepted;
+  a.status = h->status;
+  a.target_row_stride = a.draft_row_stride = V;
+  return mk_verify(&a, stream);
 }
 
 extern "C" int mk_get_status(mk_handle *h, void *stream) {

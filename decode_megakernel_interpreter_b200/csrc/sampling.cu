@@ -54,7 +54,7 @@ __device__ __forceinline__ float4 four(const T *z) {  // 16-bit types
 // memory; a vocabulary too large for that (kN = 0) is read three times.  Bound
 // by memory: each logit read and each probability written once.
 template <class T, int kN>
-__global__ void __launch_bounds__(kProbThreads, kN <= 8 ? 2 : 1) probs_kernel(const T *logits, long long ls, const float *temperature,
+__global__ void __launch_bounds__(kProbThreads, kN <= 8 ? 2 : 1) probs_kernel(const T *logits, long long ls, const float *temperature, int ts,
                                                              float *probs, long long ps, int vocab, int per) {
   __shared__ Part part, warp_part[kProbThreads / 32];
   cg::cluster_group cl = cg::this_cluster();
@@ -63,7 +63,7 @@ __global__ void __launch_bounds__(kProbThreads, kN <= 8 ? 2 : 1) probs_kernel(co
   const int v0 = min(rank * per, vocab), n = min(per, vocab - v0);
   const T *z = logits + row * ls + v0;
   float *out = probs + row * ps + v0;
-  const float t = temperature ? temperature[row] : 1.f;
+  const float t = temperature ? temperature[row * ts] : 1.f;
   const bool greedy = t == 0.f;
   // Rows that start on 16 (or 8) bytes in both places go four values at a time:
   // the thread's j-th four are at 4 (512 j + tid); else at 2048 j + 512 e + tid.
@@ -194,7 +194,7 @@ __global__ void __launch_bounds__(kProbThreads, kN <= 8 ? 2 : 1) probs_kernel(co
 constexpr int kStreamThreads = 512;
 constexpr int kStreamTurns = 4;  // fours that a thread loads at a time
 template <class T>
-__global__ void __launch_bounds__(kStreamThreads, 3) probs_stream_kernel(const T *logits, long long ls, const float *temperature,
+__global__ void __launch_bounds__(kStreamThreads, 3) probs_stream_kernel(const T *logits, long long ls, const float *temperature, int ts,
                                                                          float *probs, long long ps, int vocab, int per) {
   __shared__ Part part, warp_part[kStreamThreads / 32];
   cg::cluster_group cl = cg::this_cluster();
@@ -203,7 +203,7 @@ __global__ void __launch_bounds__(kStreamThreads, 3) probs_stream_kernel(const T
   const int v0 = min(rank * per, vocab), n = min(per, vocab - v0);
   const T *z = logits + row * ls + v0;
   float *out = probs + row * ps + v0;
-  const float t = temperature ? temperature[row] : 1.f;
+  const float t = temperature ? temperature[row * ts] : 1.f;
   const bool greedy = t == 0.f;
   const int bad_t = !(t >= 0.f && t < INFINITY);
   const float c = greedy || bad_t ? 0.f : (float)(1.4426950408889634 / (double)t);
@@ -513,14 +513,14 @@ using namespace mk;
 
 namespace {
 template <class T>
-int launch_probs(const void *logits, int64_t ls, const float *temperature, float *probs, int64_t ps, int n, int vocab,
+int launch_probs(const void *logits, int64_t ls, const float *temperature, int ts, float *probs, int64_t ps, int n, int vocab,
                  cudaStream_t st) {
   // A cluster of 8 for a large vocabulary, so that few rows still use many SMs
   // and a slice fits into registers (up to 64 values a thread).
   const int C = vocab >= 16384 ? 8 : 1;
   const int per = ((vocab + C - 1) / C + 15) / 16 * 16;
   const int turns = (per + 4 * kProbThreads - 1) / (4 * kProbThreads);
-  void (*fn)(const T *, long long, const float *, float *, long long, int, int) =
+  void (*fn)(const T *, long long, const float *, int, float *, long long, int, int) =
       turns <= 2 ? probs_kernel<T, 2> : turns <= 4 ? probs_kernel<T, 4> : turns <= 8 ? probs_kernel<T, 8> :
       turns <= 16 ? probs_kernel<T, 16> : probs_kernel<T, 0>;
   int sms = 0, rc = serve_sms(&sms);
@@ -528,25 +528,30 @@ int launch_probs(const void *logits, int64_t ls, const float *temperature, float
   if (vocab >= 16384 && (long long)n * C > 2 * sms) {
     const int few = 4, slice = ((vocab + few - 1) / few + 15) / 16 * 16;
     return serve_launch(probs_stream_kernel<T>, dim3((unsigned)n * few), kStreamThreads, 0, st, false, few, (const T *)logits,
-                        (long long)ls, temperature, probs, (long long)ps, vocab, slice);
+                        (long long)ls, temperature, ts, probs, (long long)ps, vocab, slice);
   }
   return serve_launch(fn, dim3((unsigned)n * C), kProbThreads, 0, st, false, C, (const T *)logits, (long long)ls,
-                      temperature, probs, (long long)ps, vocab, per);
+                      temperature, ts, probs, (long long)ps, vocab, per);
 }
 }  // namespace
 
-extern "C" int mk_token_probs(const void *logits, int32_t dtype, int64_t logits_stride, const float *temperature,
-                              float *probs, int64_t probs_stride, int32_t n, int32_t vocab, void *stream) {
+int mk::token_probs(const void *logits, int32_t dtype, int64_t logits_stride, const float *temperature, int ts,
+                    float *probs, int64_t probs_stride, int32_t n, int32_t vocab, void *stream) {
   if (!logits || !probs || n < 1 || vocab < 1 || vocab >= (1 << 30) || n > (1 << 24) || logits_stride < 0 ||
       probs_stride < 0 || (n > 1 && probs_stride < vocab))
     return MK_ERR_INVALID_ARG;
   cudaStream_t st = (cudaStream_t)stream;
   switch (dtype) {
-    case MK_DTYPE_F32: return launch_probs<float>(logits, logits_stride, temperature, probs, probs_stride, n, vocab, st);
-    case MK_DTYPE_BF16: return launch_probs<__nv_bfloat16>(logits, logits_stride, temperature, probs, probs_stride, n, vocab, st);
-    case MK_DTYPE_F16: return launch_probs<__half>(logits, logits_stride, temperature, probs, probs_stride, n, vocab, st);
+    case MK_DTYPE_F32: return launch_probs<float>(logits, logits_stride, temperature, ts, probs, probs_stride, n, vocab, st);
+    case MK_DTYPE_BF16: return launch_probs<__nv_bfloat16>(logits, logits_stride, temperature, ts, probs, probs_stride, n, vocab, st);
+    case MK_DTYPE_F16: return launch_probs<__half>(logits, logits_stride, temperature, ts, probs, probs_stride, n, vocab, st);
   }
   return MK_ERR_INVALID_ARG;
+}
+
+extern "C" int mk_token_probs(const void *logits, int32_t dtype, int64_t logits_stride, const float *temperature,
+                              float *probs, int64_t probs_stride, int32_t n, int32_t vocab, void *stream) {
+  return token_probs(logits, dtype, logits_stride, temperature, 1, probs, probs_stride, n, vocab, stream);
 }
 
 extern "C" int mk_verify(const mk_verify_args *a, void *stream) {

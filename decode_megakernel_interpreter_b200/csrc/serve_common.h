@@ -78,19 +78,27 @@ inline int serve_allow_smem(std::atomic<uint64_t> &done, const void *fn, size_t 
   return MK_OK;
 }
 
+// mk_token_probs with the temperatures `ts` words apart (0: one for all rows).
+int token_probs(const void *logits, int32_t dtype, int64_t logits_stride, const float *temperature, int ts, float *probs,
+                int64_t probs_stride, int32_t n, int32_t vocab, void *stream);
+
+// mk_attn_shared inside an engine's step (bf16 cache, one token a sequence, scale
+// above 0): a->q is the step's q and `out` its attention output, both tagged
+// 32-bit words [batch][n_q_heads][head_dim]; a->out is not used (but not NULL).
+int attn_shared_tagged(const mk_attn_shared_args *a, float *out, const unsigned *epoch, void *workspace, void *stream);
+
 inline bool aligned_to(const void *p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
 
 #ifdef __CUDACC__
-namespace {
 // The kernel before this one on the stream has finished and its writes are visible.
-__device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+static __device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 // The next kernel's blocks may be scheduled.
-__device__ __forceinline__ void pdl_trigger() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+static __device__ __forceinline__ void pdl_trigger() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 // First code wins.
-__device__ __forceinline__ void report(int32_t *status, int code) {
+static __device__ __forceinline__ void report(int32_t *status, int code) {
   if (status) atomicCAS(status, 0, code);
 }
-__device__ __forceinline__ int warp_incl_sum(int v) {
+static __device__ __forceinline__ int warp_incl_sum(int v) {
   const int lane = threadIdx.x & 31;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
@@ -99,7 +107,6 @@ __device__ __forceinline__ int warp_incl_sum(int v) {
   }
   return v;
 }
-}  // namespace
 #endif
 
 }  // namespace mk

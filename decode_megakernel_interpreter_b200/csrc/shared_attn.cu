@@ -57,6 +57,9 @@ struct AttnDev {
   // of the tensor cores' (for items that have work)
   int *how;
   int2 *who, *tc_who;
+  // an engine's own step (kFull): q and the output are tagged 32-bit words [batch][n_q_heads][d]
+  float *tagged;
+  const unsigned *epoch;
   float inv_G, inv_T;
   // the prefix on the tensor cores (tc_rows > 0; n_prefix_items is 0 then):
   // items [kv head][group of tc_rows rows]
@@ -229,6 +232,16 @@ struct Num<__half> {
   }
 };
 
+// Two numbers as the type's nearest, and what that leaves as another.
+template <class T>
+__device__ __forceinline__ void two_parts(float2 x, uint32_t &hi, uint32_t &lo) {
+  hi = Num<T>::pack(x.x, x.y);
+  const float2 r = Num<T>::unpack(hi);
+  lo = Num<T>::pack(x.x - r.x, x.y - r.y);
+}
+// The values of an engine's tagged words (the two low bits are the tag).
+__device__ __forceinline__ float2 untag(uint2 w) { return make_float2(__uint_as_float(w.x & ~3u), __uint_as_float(w.y & ~3u)); }
+
 // Shared memory of the small items: each warp's stages (a unit's rows of K, then
 // of V); then the line's sums.
 template <int D>
@@ -300,7 +313,7 @@ __device__ __forceinline__ void copy_rows(const AttnDev &p, const char *k, const
 // is how many of them wait for memory at once: 12 warps an SM, each with the
 // next unit in flight.  They come before the prefix, whose partials are the
 // larger ones: the join then finds those in L2.
-template <class T, int D>
+template <class T, int D, bool kFull>
 __device__ __forceinline__ void small_items(const AttnDev &p, char *sm, int *red) {
   int *sum = reinterpret_cast<int *>(sm + smem_stages<D>());
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -376,7 +389,7 @@ __device__ __forceinline__ void small_items(const AttnDev &p, char *sm, int *red
     int ahead = look_up(1);
 
     // ---- this thread's rows: r and r + 8 of the tile (r = lane / 4)
-    uint32_t qf[D / 16][4];
+    uint32_t qf[D / 16][4], ql[kFull ? D / 16 : 1][4];
     int sees[2], min_sees = hi;  // positions that the row sees
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
@@ -390,10 +403,20 @@ __device__ __forceinline__ void small_items(const AttnDev &p, char *sm, int *red
         qp = p.q + rb * p.q_bs + rt * p.q_ts + rh * p.q_hs;
         min_sees = min(min_sees, sees[h]);
       }
+      if (kFull) {
 #pragma unroll
-      for (int k = 0; k < D / 16; ++k) {
-        qf[k][h] = qp ? *reinterpret_cast<const uint32_t *>(qp + (k * 16 + (lane & 3) * 2) * 2) ^ p.flip : 0u;
-        qf[k][h + 2] = qp ? *reinterpret_cast<const uint32_t *>(qp + (k * 16 + 8 + (lane & 3) * 2) * 2) ^ p.flip : 0u;
+        for (int k = 0; k < D / 16; ++k)
+#pragma unroll
+          for (int x = 0; x < 2; ++x) {
+            const float2 y = qp ? untag(*reinterpret_cast<const uint2 *>(qp + (k * 16 + x * 8 + (lane & 3) * 2) * 4)) : make_float2(0.f, 0.f);
+            two_parts<T>(y, qf[k][h + 2 * x], ql[k][h + 2 * x]);
+          }
+      } else {
+#pragma unroll
+        for (int k = 0; k < D / 16; ++k) {
+          qf[k][h] = qp ? *reinterpret_cast<const uint32_t *>(qp + (k * 16 + (lane & 3) * 2) * 2) ^ p.flip : 0u;
+          qf[k][h + 2] = qp ? *reinterpret_cast<const uint32_t *>(qp + (k * 16 + 8 + (lane & 3) * 2) * 2) ^ p.flip : 0u;
+        }
       }
     }
     min_sees = __reduce_min_sync(0xffffffffu, min_sees);
@@ -420,6 +443,10 @@ __device__ __forceinline__ void small_items(const AttnDev &p, char *sm, int *red
         ldsm4(kf, ka + at<D>((lane & 7) + (lane >> 4) * 8, k * 2 + ((lane >> 3) & 1)));
         Num<T>::mma(s[0], qf[k], kf[0], kf[1]);
         Num<T>::mma(s[1], qf[k], kf[2], kf[3]);
+        if (kFull) {
+          Num<T>::mma(s[0], ql[k], kf[0], kf[1]);
+          Num<T>::mma(s[1], ql[k], kf[2], kf[3]);
+        }
       }
       const bool edge = pos0 < lo || pos0 + kUnit > min(min_sees, hi);
       if (edge) {
@@ -503,11 +530,8 @@ __device__ __forceinline__ void small_items(const AttnDev &p, char *sm, int *red
 #pragma unroll
       for (int n = 0; n < 2; ++n)
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          ph[2 * n + h] = Num<T>::pack(s[n][2 * h], s[n][2 * h + 1]);
-          const float2 r = Num<T>::unpack(ph[2 * n + h]);
-          pl[2 * n + h] = Num<T>::pack(s[n][2 * h] - r.x, s[n][2 * h + 1] - r.y);
-        }
+        for (int h = 0; h < 2; ++h)
+          two_parts<T>(make_float2(s[n][2 * h], s[n][2 * h + 1]), ph[2 * n + h], pl[2 * n + h]);
 #pragma unroll
       for (int d = 0; d < D / 16; ++d) {
         uint32_t vf[4];  // positions 0-7 and 8-15 of columns 0-7, then of columns 8-15
@@ -553,7 +577,9 @@ __device__ __forceinline__ void small_items(const AttnDev &p, char *sm, int *red
 // half issues its matrix instructions (one warp for both spent longer on the
 // waits and descriptors than the instructions took).
 // P takes S's place in tensor memory, rounded to the operands' type: half a
-// step (2^-8 or 2^-11) of each weight, as the output's own rounding.
+// step (2^-8 or 2^-11) of each weight, as the output's own rounding.  With kFull
+// Q and P are two numbers of the type each, the second what the first leaves,
+// for an engine whose q and attention output are 32-bit numbers.
 
 constexpr int kTcRows = 128;  // rows of a half
 constexpr int kTcKeys = 64;   // positions of a tile
@@ -565,12 +591,16 @@ constexpr int tc_tile() {
   return kTcKeys * D * 2;
 }
 template <int D>
-constexpr int tc_ring() {
-  return D == 128 ? 10 : 16;  // tiles of K or V in flight or in use
+constexpr int tc_q() {  // a half's rows of Q
+  return kTcRows * D * 2;
 }
-template <int D>
+template <int D, bool kFull>
+constexpr int tc_ring() {
+  return D == 64 ? 16 : kFull ? 6 : 10;  // tiles of K or V in flight or in use
+}
+template <int D, bool kFull>
 constexpr int tc_smem() {
-  return 2 * kTcRows * D * 2 + tc_ring<D>() * tc_tile<D>() + 1024;
+  return (kFull ? 4 : 2) * tc_q<D>() + tc_ring<D, kFull>() * tc_tile<D>() + 1024;
 }
 
 // Byte of element chunk c (8 elements) of row r in a tile of `rows` rows: 64
@@ -745,17 +775,17 @@ struct TcLine {
   }
 };
 
-template <class T, int D>
+template <class T, int D, bool kFull>
 __global__ void __launch_bounds__(kTcThreads, 1)
     attn_kernel(const AttnDev p, const __grid_constant__ CUtensorMap k_map, const __grid_constant__ CUtensorMap v_map) {
   extern __shared__ char sm_raw[];
   __shared__ TcShared sh;
-  constexpr int kRing = tc_ring<D>();
+  constexpr int kRing = tc_ring<D, kFull>();
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   __shared__ int red[kWarps];
   const uint32_t base = (smem_addr(sm_raw) + 1023) & ~1023u;
   char *sm = sm_raw + (base - smem_addr(sm_raw));
-  const uint32_t ring = base + 2 * kTcRows * D * 2;
+  const uint32_t ring = base + (kFull ? 4 : 2) * tc_q<D>();  // Q of both halves, then what it leaves
   const bool pair = p.tc_rows == 2 * kTcRows;  // the halves have rows of their own
   if (tid == 0) {
     for (int i = 0; i < kRing; ++i) {
@@ -779,7 +809,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_addr(&sh.tmem)) : "memory");
   pdl_wait();
   pdl_trigger();
-  small_items<T, D>(p, sm, red);
+  small_items<T, D, kFull>(p, sm, red);
   cp_wait<0>();
   fence_smem_async();  // the tensor copies reuse the small items' stages
   tc_before();
@@ -874,7 +904,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     constexpr uint32_t kS = (1u << 4) | (kType << 7) | (kType << 10) | ((kTcKeys / 8u) << 17) | ((128u / 16) << 24);
     constexpr uint32_t kO = (1u << 4) | (kType << 7) | (kType << 10) | (1u << 16) | ((uint32_t)(D / 8) << 17) | ((128u / 16) << 24);
     const int w = warp - 10;
-    const uint32_t q_low = tc_low(base, 16) + w * (kTcRows * D * 2 >> 4);
+    const uint32_t q_low = tc_low(base, 16) + w * (tc_q<D>() >> 4);
     const uint32_t k_low = tc_low(ring, 16), v_low = tc_low(ring, kTcKeys * 128);
     int g = 0;                          // ring entries before this item
     uint32_t q_phase = 0, p_phase = 0;  // one bit; bit i
@@ -892,6 +922,11 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         for (int e = 0; e < D / 16; ++e)
           mma_ss(s_of(w, i), tc_desc(q_low + (e / 4 * (kTcRows * 128) + e % 4 * 32 >> 4)),
                  tc_desc(k + (e / 4 * (kTcKeys * 128) + e % 4 * 32 >> 4)), kS, e > 0);
+        if (kFull)
+#pragma unroll
+          for (int e = 0; e < D / 16; ++e)
+            mma_ss(s_of(w, i), tc_desc(q_low + (2 * tc_q<D>() + e / 4 * (kTcRows * 128) + e % 4 * 32 >> 4)),
+                   tc_desc(k + (e / 4 * (kTcKeys * 128) + e % 4 * 32 >> 4)), kS, true);
         mma_commit(&sh.s_full[w][i]);
         mma_commit(&sh.empty[x]);
       }
@@ -931,6 +966,10 @@ __global__ void __launch_bounds__(kTcThreads, 1)
 #pragma unroll
             for (int e = 0; e < kTcKeys / 16; ++e)
               mma_ts(o_of(w), s_of(w, i) + e * 8, tc_desc(low + e * (2048 >> 4)), kO, j > j0 || e > 0);
+            if (kFull)
+#pragma unroll
+              for (int e = 0; e < kTcKeys / 16; ++e)
+                mma_ts(o_of(w), s_of(w, i) + 32 + e * 8, tc_desc(low + e * (2048 >> 4)), kO, true);
             mma_commit(&sh.o_full[w]);
             mma_commit(&sh.empty[v]);
           }
@@ -969,17 +1008,26 @@ __global__ void __launch_bounds__(kTcThreads, 1)
           const int rh = kv * p.G + row % p.G, rt = row / p.G % p.T, rb = row / p.G / p.T;
           qp = p.q + rb * p.q_bs + rt * p.q_ts + rh * p.q_hs;
         }
-#pragma unroll 8
+        char *const q_to = sm + w * tc_q<D>();
+#pragma unroll 4
         for (int i = 0; i < D / 8; ++i) {
-          uint4 x = make_uint4(0, 0, 0, 0);
-          if (live) {
+          uint4 x = make_uint4(0, 0, 0, 0), rest = x;
+          if (live && kFull) {
+            const uint4 *f = reinterpret_cast<const uint4 *>(qp + i * 32);
+            const uint4 f0 = f[0], f1 = f[1];
+            two_parts<T>(untag(make_uint2(f0.x, f0.y)), x.x, rest.x);
+            two_parts<T>(untag(make_uint2(f0.z, f0.w)), x.y, rest.y);
+            two_parts<T>(untag(make_uint2(f1.x, f1.y)), x.z, rest.z);
+            two_parts<T>(untag(make_uint2(f1.z, f1.w)), x.w, rest.w);
+          } else if (live) {
             x = *reinterpret_cast<const uint4 *>(qp + i * 16);
             x.x ^= p.flip;
             x.y ^= p.flip;
             x.z ^= p.flip;
             x.w ^= p.flip;
           }
-          *reinterpret_cast<uint4 *>(sm + w * (kTcRows * D * 2) + tc_at(kTcRows, r, i)) = x;
+          *reinterpret_cast<uint4 *>(q_to + tc_at(kTcRows, r, i)) = x;
+          if (kFull) *reinterpret_cast<uint4 *>(q_to + 2 * tc_q<D>() + tc_at(kTcRows, r, i)) = rest;
         }
         fence_smem_async();
         __syncwarp();
@@ -1007,7 +1055,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
           // The weights are first taken with the maximum so far, while this
           // tile's own is found; where that has grown too much (and in an
           // item's first tile), once more.
-          uint32_t h[32];
+          uint32_t h[32], g[kFull ? 32 : 1];
           unsigned long long sum;
           for (;;) {
             const float b = m == -INFINITY ? 0.f : m;
@@ -1022,7 +1070,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
               const float2 y = unpack2(fma2(pack2(x0, x1), scale, minus));
               const float e0 = exp2_(y.x), e1 = exp2_(y.y);
               sum = add2(sum, pack2(e0, e1));
-              h[e / 2] = Num<T>::pack(e0, e1);
+              if (kFull) two_parts<T>(make_float2(e0, e1), h[e / 2], g[kFull ? e / 2 : 0]);
+              else h[e / 2] = Num<T>::pack(e0, e1);
             }
             const float top = fmaxf(fmaxf(t[0], t[1]), fmaxf(t[2], t[3])) * p.scale2;
             const bool grow = top > (m == -INFINITY ? m : m + kGrow);
@@ -1049,6 +1098,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
           }
           if (!ok) break;
           tm_st32(s, h);
+          if constexpr (kFull) tm_st32(s + 32, g);
           const float2 both = unpack2(sum);
           l += both.x + both.y;
           tm_wait_st();
@@ -1103,7 +1153,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
 constexpr int kJoinRows = 8;
 constexpr int kJoinThreads = 512;
 constexpr int kJoinMax = 512;  // partials of a row whose weights are kept at a time
-template <class T, int D>
+template <class T, int D, bool kFull>
 __global__ void __launch_bounds__(kJoinThreads) join_kernel(const AttnDev p) {
   __shared__ float w_s[kJoinMax][kJoinRows], m_s[kJoinThreads / 32][kJoinRows], l_s[kJoinThreads / 32][kJoinRows];
   __shared__ float4 a_s[3][D / 4][kJoinRows];
@@ -1223,6 +1273,14 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const AttnDev p) {
           a[k].z += z.z;
           a[k].w += z.w;
         }
+        if (kFull) {
+          // rounded to 22 bits, the step number in the two low ones
+          const unsigned tag = *p.epoch & 3u;
+          auto word = [&](float x) { return ((__float_as_uint(x * inv) + 2u) & ~3u) | tag; };
+          reinterpret_cast<uint4 *>(p.tagged + ((long long)b * p.nq + kv * p.G + g) * D)[d0 + 4 * k] =
+              make_uint4(word(a[k].x), word(a[k].y), word(a[k].z), word(a[k].w));
+          continue;
+        }
         *reinterpret_cast<uint2 *>(op + k * 32) = make_uint2(Num<T>::pack(a[k].x * inv, a[k].y * inv), Num<T>::pack(a[k].z * inv, a[k].w * inv));
       }
       if (p.lse && d0 == 0)
@@ -1303,15 +1361,15 @@ Sizes sizes_of(const AttnDev &d, int head_dim, int sms) {
   return Sizes{rows * head_dim * 4, rows * 8, tc * head_dim * 4, tc * 8, 8 * (int64_t)d.n_items, 8 * (int64_t)d.nkv * d.tc_groups, 4 * (int64_t)d.B};
 }
 
-template <class T, int D>
+template <class T, int D, bool kFull = false>
 int launch(const AttnDev &p, const CUtensorMap (&maps)[2], int sms, cudaStream_t st) {
-  static_assert(smem_stages<D>() + 4 * (kMaxRowsB + 1) + 1024 <= tc_smem<D>(), "the small items' stages and sums fit");
+  static_assert(smem_stages<D>() + 4 * (kMaxRowsB + 1) + 1024 <= tc_smem<D, kFull>(), "the small items' stages and sums fit");
   static std::atomic<uint64_t> allowed;
-  int rc = serve_allow_smem(allowed, (const void *)attn_kernel<T, D>, tc_smem<D>());
-  if (!rc) rc = serve_launch(attn_kernel<T, D>, dim3(sms), kTcThreads, tc_smem<D>(), st, false, 1, p, maps[0], maps[1]);
+  int rc = serve_allow_smem(allowed, (const void *)attn_kernel<T, D, kFull>, tc_smem<D, kFull>());
+  if (!rc) rc = serve_launch(attn_kernel<T, D, kFull>, dim3(sms), kTcThreads, tc_smem<D, kFull>(), st, false, 1, p, maps[0], maps[1]);
   if (rc) return rc;
   const dim3 grid((p.B * p.T * p.G + kJoinRows - 1) / kJoinRows, p.nkv);
-  return serve_launch(join_kernel<T, D>, grid, kJoinThreads, 0, st, true, 1, p);
+  return serve_launch(join_kernel<T, D, kFull>, grid, kJoinThreads, 0, st, true, 1, p);
 }
 
 }  // namespace
@@ -1329,7 +1387,9 @@ extern "C" int64_t mk_attn_shared_workspace_bytes(const mk_attn_shared_args *a) 
   return z.part_o + z.part_ml + z.tc_o + z.tc_ml + z.who + z.tc_who + z.how;
 }
 
-extern "C" int mk_attn_shared(const mk_attn_shared_args *a, void *workspace, void *stream) {
+// mk_attn_shared; with `tagged`, q is an engine's buffer of tagged words
+// [batch][n_q_heads][d] and the output goes to `tagged`, with the step's tag.
+static int attn_shared(const mk_attn_shared_args *a, float *tagged, const unsigned *epoch, void *workspace, void *stream) {
   int rc = check(a);
   if (rc) return rc;
   if (!a->q || !a->k || !a->v || !a->out || !a->table || !a->lens || !workspace || !aligned_to(workspace, 256) ||
@@ -1394,7 +1454,23 @@ extern "C" int mk_attn_shared(const mk_attn_shared_args *a, void *workspace, voi
     if (make_map(&maps[0], a, a->k, rows) && make_map(&maps[1], a, a->v, rows)) d.box = rows;
   }
   cudaStream_t st = (cudaStream_t)stream;
+  if (tagged) {
+    d.tagged = tagged;
+    d.epoch = epoch;
+    d.q_bs = 4 * a->q_batch_stride;
+    d.q_ts = 4 * a->q_token_stride;
+    d.q_hs = 4 * a->q_head_stride;
+    return a->head_dim == 64 ? launch<__nv_bfloat16, 64, true>(d, maps, sms, st) : launch<__nv_bfloat16, 128, true>(d, maps, sms, st);
+  }
   if (a->dtype == MK_DTYPE_BF16)
     return a->head_dim == 64 ? launch<__nv_bfloat16, 64>(d, maps, sms, st) : launch<__nv_bfloat16, 128>(d, maps, sms, st);
   return a->head_dim == 64 ? launch<__half, 64>(d, maps, sms, st) : launch<__half, 128>(d, maps, sms, st);
+}
+
+extern "C" int mk_attn_shared(const mk_attn_shared_args *a, void *workspace, void *stream) {
+  return attn_shared(a, nullptr, nullptr, workspace, stream);
+}
+
+int mk::attn_shared_tagged(const mk_attn_shared_args *a, float *out, const unsigned *epoch, void *workspace, void *stream) {
+  return attn_shared(a, out, epoch, workspace, stream);
 }

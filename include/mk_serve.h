@@ -254,6 +254,48 @@ typedef struct {
 
 int mk_verify(const mk_verify_args *a, void *stream);
 
+/* ------------------------------------------------------------------ with an engine */
+/*
+ * mk_speculate: check drafted tokens of one sequence with an engine, and sample
+ * the token after those that stand: mk_prefill of the n_tokens given tokens
+ * with every row's logits kept, mk_token_probs of those rows, mk_verify.
+ *  - tokens: device int32 [n_tokens]: the sequence's last token, at position
+ *    pos0, then n_tokens - 1 drafted ones; 1 <= n_tokens <= 16.  (n_tokens = 1
+ *    samples the next token.)  Their K/V rows are written; those of tokens that
+ *    do not stand are overwritten by the call that continues at
+ *    pos0 + accepted + 1.
+ *  - draft_probs: device float [n_tokens - 1][vocab] probabilities of the
+ *    drafter, or NULL.  temperature: device float, one word, or NULL (1); 0 is
+ *    greedy.  u: device float [n_tokens] in [0, 1), the last for the sampling.
+ *  - out_tokens: device int32 [n_tokens] as mk_verify's; n_accepted: device
+ *    int32, one word.
+ *  - As for mk_prefill: a plan that runs as one launch a step; a batched plan
+ *    takes all tokens in one launch, a batch-1 plan one launch a token.  The
+ *    first call after mk_plan allocates scratch (not while capturing).
+ *  - Errors: MK_ERR_INVALID_ARG, MK_ERR_NOT_PLANNED, MK_ERR_OUT_OF_MEMORY,
+ *    MK_ERR_LAUNCH, MK_ERR_CUDA; device-side ones by mk_get_status.
+ */
+int mk_speculate(mk_handle *h, int32_t seq, const int32_t *tokens, int32_t n_tokens, int32_t pos0,
+                 const float *draft_probs, const float *temperature, const float *u,
+                 int32_t *out_tokens, int32_t *n_accepted, void *stream);
+
+/*
+ * mk_decode_step_shared: mk_decode_step for sequences that share their first
+ * prefix_len positions, whose keys and values are read, once for the batch,
+ * from sequence prefix_seq's rows of the cache (the kernels of mk_attn_shared in
+ * the place of the attention instructions, on the step's 32-bit q and output).
+ * Sequence b holds only its own rows prefix_len .. positions[b].
+ *  - Needs a plan with exec_mode MK_EXEC_PER_OP (one launch per instruction
+ *    class), MK_ERR_INVALID_ARG otherwise.  0 <= prefix_len <= max_seq; a
+ *    position below prefix_len is reported as MK_ERR_DEVICE_INPUT.
+ *  - The other arguments and errors as for mk_decode_step.  The first call
+ *    after mk_plan allocates scratch (not while capturing).  Steps of both
+ *    kinds may follow one another.
+ */
+int mk_decode_step_shared(mk_handle *h, const int32_t *tokens, const int32_t *positions,
+                          int32_t prefix_seq, int32_t prefix_len, float *logits_out,
+                          int32_t *next_tokens_out, void *stream);
+
 #ifdef __cplusplus
 }
 #endif

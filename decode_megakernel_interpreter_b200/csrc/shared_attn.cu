@@ -790,7 +790,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   if (tid == 0) {
     for (int i = 0; i < kRing; ++i) {
       bar_init(&sh.full[i], 64);
-      bar_init(&sh.empty[i], pair ? 2 : 1);
+      bar_init(&sh.empty[i], 2);  // both halves pass every entry
     }
     for (int w = 0; w < 2; ++w) {
       bar_init(&sh.q_full[w], 4);
@@ -909,7 +909,17 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     int g = 0;                          // ring entries before this item
     uint32_t q_phase = 0, p_phase = 0;  // one bit; bit i
     bool ok = true;
-    auto take = [&](int e) {  // entry e's tile has landed
+    int seen = 0;                       // entries of this item taken or passed
+    // Entry e's tile has landed.  The entries before it that are the other
+    // half's are passed: waited for and let go, so that a slot's phase is never
+    // more than one ahead of, or behind, either half.
+    auto take = [&](int e) {
+      for (; ok && seen < e; ++seen) {
+        const int x = (g + seen) % kRing;
+        ok = bar_wait_all(&sh, &sh.full[x], ((g + seen) / kRing) & 1, p.status);
+        if (ok && lane == 0) bar_arrive(&sh.empty[x]);
+      }
+      seen = e + 1;
       const int x = (g + e) % kRing;
       ok = ok && bar_wait_all(&sh, &sh.full[x], ((g + e) / kRing) & 1, p.status);
       fence_smem_async();  // the copies' writes, before the tensor cores' reads
@@ -940,14 +950,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       const TcOrder order{n, min(dist, n)};
       // this half's tiles: all (pair) or every other; its k-th S is in buffer k & 1
       const int step = pair ? 1 : 2, j0 = pair ? 0 : w;
-      if (item % p.tc_groups * p.tc_rows + (pair ? w * kTcRows : 0) >= R) {
-        // no rows: the tiles only pass
-        for (int e = 0; ok && e < 2 * n; ++e) {
-          const int x = take(e);
-          if (ok && elect_one()) mma_commit(&sh.empty[x]);
-          __syncwarp();
-        }
-      } else if (j0 < n) {
+      seen = 0;
+      if (item % p.tc_groups * p.tc_rows + (pair ? w * kTcRows : 0) < R && j0 < n) {  // (else the tiles only pass)
         ok = ok && bar_wait_all(&sh, &sh.q_full[w], q_phase, p.status);
         q_phase ^= 1;
         for (int k = 0; ok && k < 2 && j0 + k * step < n; ++k) {
@@ -979,6 +983,11 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             if (ok) scores(i, x);
           }
         }
+      }
+      for (; ok && seen < 2 * n; ++seen) {
+        const int x = (g + seen) % kRing;
+        ok = bar_wait_all(&sh, &sh.full[x], ((g + seen) / kRing) & 1, p.status);
+        if (ok && lane == 0) bar_arrive(&sh.empty[x]);
       }
       g += 2 * n;
     }
@@ -1103,6 +1112,11 @@ __global__ void __launch_bounds__(kTcThreads, 1)
           l += both.x + both.y;
           tm_wait_st();
         }
+        // The item's end waits for its last P V; a phase's parity only tells it
+        // from the one before if that one is known to be complete, which it is
+        // to be before the last P is handed over.
+        if (j + step >= n && done > 0) ok = bar_wait_all(&sh, &sh.o_full[w], (done - 1) & 1, p.status);
+        if (!ok) break;
         tc_before();
         __syncwarp();
         if (lane == 0) bar_arrive(&sh.p_full[w][i]);

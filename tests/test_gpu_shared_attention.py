@@ -90,6 +90,36 @@ def test_long_prefix():
     check(case(9, 2, 8, 2, 128, 64, 4001, [4003 + 5 * b for b in range(9)]))
 
 
+@pytest.mark.parametrize("dtype", [BF16, F16])
+@pytest.mark.parametrize("B, T, nq, nkv, d, page, prefix", [
+    (16, 1, 32, 8, 64, 64, 16000), (16, 1, 32, 8, 64, 50, 11000), (64, 1, 32, 8, 64, 16, 20011), (16, 1, 32, 8, 128, 64, 9001),
+    (64, 1, 32, 8, 128, 96, 16000), (5, 8, 8, 2, 128, 32, 70001), (3, 1, 4, 4, 64, 64, 150000), (200, 1, 4, 1, 64, 64, 40000)])
+def test_many_tiles_per_block(B, T, nq, nkv, d, page, prefix, dtype):
+    """Prefixes of which a block takes many more tiles than it holds at a time, against 64-bit products: a row's error
+    within the bound that the shorter cases derive, with the 2-norms of p v and v in the place of single elements."""
+    c = case(B, T, nq, nkv, d, page, prefix, [prefix + T + 3 * (b % 9) for b in range(B)], dtype)
+    h = torch.finfo(dtype).eps / 2
+    for _ in range(3):  # (a race would not fail every time)
+        (out, lse), status = run(c)
+        assert status == 0
+        for b in (0, B // 2, B - 1):
+            n = int(c["lens"][b])
+            at = torch.arange(n, device="cuda")
+            pages = torch.where(at < prefix, c["prefix_pages"][at.clamp(max=prefix - 1) // page].long(), c["table"][b, at // page].long())
+            K, V = (c[x][pages, :, at % page].double().transpose(0, 1) for x in ("k", "v"))
+            for t in (0, T - 1):
+                m = n - (T - 1 - t)
+                q = c["q"][b, t].double().view(nkv, nq // nkv, d)
+                s = torch.einsum("hgd,hnd->hgn", q, K[:, :m]) / math.sqrt(d)
+                p = s.softmax(-1)
+                o = torch.einsum("hgn,hnd->hgd", p, V[:, :m])
+                spread = torch.einsum("hgn,hnd->hgd", p * p, V[:, :m] ** 2).sum(-1).sqrt()  # of independent roundings of p
+                err = (out[b, t].double().view_as(o) - o).norm(dim=-1)
+                assert (err <= h * (o.norm(dim=-1) + 4 * spread) + 1e-4 * o.norm(dim=-1)).all(), (b, t, float(err.max()))
+                z = torch.logsumexp(s, -1)
+                assert ((lse[b, t].double().view_as(z) - z).abs() <= 1e-4).all()
+
+
 def test_only_a_prefix_and_only_own():
     check(case(3, 1, 4, 2, 64, 16, 77, [77, 77, 77]))
     check(case(3, 1, 4, 2, 64, 16, 0, [1, 64, 77]))

@@ -65,7 +65,6 @@ struct mk_handle {
   // call, its workspace
   int *sh_words = nullptr;  // [0] prefix page, [1] prefix length, then lens[B], table[B]
   void *sh_ws = nullptr;
-  bool sh_skipped = false;  // the attention instructions did not run in the last step
   int last_detail[6] = {0, 0, 0, 0, 0, 0};
   // per-op graph mode
   cudaGraphExec_t gexec = nullptr;
@@ -496,7 +495,6 @@ static void drop_plan(mk_handle *h) {
   h->sp_next = nullptr;
   h->sh_words = nullptr;
   h->sh_ws = nullptr;
-  h->sh_skipped = false;
   h->planned = false;
 }
 
@@ -770,10 +768,10 @@ extern "C" int mk_plan(mk_handle *h, const mk_plan_opts *opts_in) {
   return MK_OK;
 }
 
-// What a step whose attention instructions did not run left behind: a merge
-// ticket behind the step number, and tagged partials that are older than the one
-// step which their 2-bit tags tell apart.  Both as the last step would have left
-// them.
+// A step whose attention instructions did not run leaves merge tickets behind the
+// step number, and tagged partials older than the one step which their 2-bit
+// tags tell apart.  Both as the step would have left them, so that steps of both
+// kinds (and graphs of either) may follow one another in any order.
 static __global__ void resync_attn_kernel(KParams k) {
   const unsigned epoch = *k.epoch;
   const long long n = (long long)k.L * k.B * k.nq * k.S * k.d, i0 = blockIdx.x * (long long)blockDim.x + threadIdx.x;
@@ -830,16 +828,9 @@ static int shared_attention(mk_handle *h, const KParams &k, int l, cudaStream_t 
 }
 
 static int launch_per_op(mk_handle *h, KParams k, cudaStream_t st, bool shared = false) {
-  if (!shared && h->sh_skipped) {
-    resync_attn_kernel<<<4 * h->sm_count, 256, 0, st>>>(k);
-    cudaError_t e = cudaGetLastError();
-    if (e != cudaSuccess) return cuda_code(e);
-    h->sh_skipped = false;
-  }
   const int n_stage = h->shape.L * kStagesPerLayer + 1;
   for (int sidx = 0; sidx < n_stage; ++sidx) {
     if (shared && sidx < n_stage - 1 && sidx % kStagesPerLayer == ST_ATTN) {
-      h->sh_skipped = true;
       const int rc = shared_attention(h, k, sidx / kStagesPerLayer, st);
       if (rc) return rc;
       continue;
@@ -852,6 +843,10 @@ static int launch_per_op(mk_handle *h, KParams k, cudaStream_t st, bool shared =
       cudaGetLastError();
       return cuda_code(e);
     }
+  }
+  if (shared) {
+    resync_attn_kernel<<<4 * h->sm_count, 256, 0, st>>>(k);
+    return cuda_code(cudaGetLastError());
   }
   return MK_OK;
 }

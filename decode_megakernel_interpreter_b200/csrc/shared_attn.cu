@@ -84,11 +84,11 @@ struct Share {
   __device__ __forceinline__ int begin(int c) const { return c * each + c * rest / N; }
 };
 
-// positions of sequence b (negative: unused), cut to its pages
+// positions of sequence b (-1: unused), cut to its pages
 __device__ __forceinline__ int seq_len(const AttnDev &p, int b) {
   const int cap = p.table_width * p.page, n = p.lens[b];
   if (n > cap) report(p.status, MK_ERR_DEVICE_INPUT);
-  return min(n, cap);
+  return max(-1, min(n, cap));
 }
 __device__ __forceinline__ int prefix_of(const AttnDev &p) {
   const long long cap = (long long)p.n_prefix_pages * p.page, n = p.n_prefix_pages > 0 ? p.prefix_len[0] : 0;

@@ -238,6 +238,10 @@ def shared_attention(q, k, v, table, lens, prefix_pages=None, prefix_len=None, s
         if lse is None and return_lse:
             lse = q.new_empty((B, T, nq), dtype=torch.float32)
         os = out.stride()
+        # (a dimension of size 1 may come with any stride)
+        qs = [x if n > 1 else 8 for x, n in zip(qs, q.shape)]
+        os = [x if n > 1 else 8 for x, n in zip(os, q.shape)]
+        ks = [x if n > 1 else 8 for x, n in zip(ks, k.shape)]
         a = mk_attn_shared_args(
             B, T, nq, nkv, d, code, page, n_pages, n_prefix, table.shape[1],
             1.0 / math.sqrt(d) if scale is None else scale, q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(),

@@ -46,6 +46,36 @@ def test_vocabularies_and_types(V, dtype):
     check_probs(z, None, sv.token_probs(z))
 
 
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("n, V", [(40, 16384), (41, 20001), (150, 32003), (75, 50004), (38, 128256)])
+def test_many_rows(n, V, dtype):
+    """More rows than the chip holds at a time, with every kind of row among them."""
+    g = torch.Generator(device="cuda").manual_seed(V)
+    z = (4 * torch.randn(n, V, generator=g, device="cuda")).to(dtype)
+    t = 0.3 + 2 * torch.rand(n, generator=g, device="cuda")
+    t[::7] = 0
+    z[7, 5000] = z[7, 9000] = z[7].max() + 1    # greedy with a tie
+    z[3, ::2] = -math.inf
+    z[4] = -math.inf
+    z[5, V - 1] = math.nan
+    z[14, 3] = math.nan                         # greedy
+    z[6, 77] = math.inf
+    z[8, :V - 1] = -math.inf
+    t[9] = -1
+    p = sv.token_probs(z, t)
+    check_probs(z[:24], t[:24], p[:24])
+    check_probs(z[-3:], t[-3:], p[-3:])
+    assert int(p[7].argmax()) == 5000 and (p[[4, 5, 6, 9, 14]] == 0).all() and p[8, V - 1] == 1
+    if dtype is torch.float32:
+        sv.token_probs(z, t, out=z)             # in place
+        assert torch.equal(z, p)
+        big = torch.randn(n, V + 3, generator=g, device="cuda")
+        out = torch.full((n, V + 1), 7.0, device="cuda")
+        sv.token_probs(big[:, 2:V + 2], t, out=out[:, :V])
+        check_probs(big[:3, 2:V + 2], t[:3], out[:3, :V])
+        assert (out[:, V] == 7).all()
+
+
 def test_a_vocabulary_that_does_not_stay_on_chip():
     g = torch.Generator(device="cuda").manual_seed(1)
     z = torch.randn(2, 500003, generator=g, device="cuda")

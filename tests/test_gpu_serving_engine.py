@@ -198,6 +198,43 @@ def test_steps_of_both_kinds_in_turn():
         two.close()
 
 
+def test_captured_steps_of_both_kinds():
+    """Graphs of an ordinary and of a shared step, replayed in turn, against eager ordinary steps."""
+    shape, batch, prefix = SMALL_1B, 16, 100
+    hs, one, two = shared_setup(shape, batch, prefix, prefix + 64)
+    try:
+        two._keep[1].copy_(one._keep[1])
+        two._keep[2].copy_(one._keep[2])
+        one.plan(batch=batch, exec_mode="per_op")
+        two.plan(batch=batch, exec_mode="per_op")
+        la, lb = (torch.empty(batch, shape.vocab, device="cuda") for _ in range(2))
+        na, nb = ints([0] * batch), ints([0] * batch)
+        t, p = ints(list(range(batch))), ints([prefix + b for b in range(batch)])
+        two.decode_step_shared(t, p, 3, prefix, lb, nb)   # (allocates its scratch)
+        one.decode_step(t, p, la, na)
+        assert two.status() == mk.MK_OK
+        graphs = {}
+        for kind in "os":
+            g = torch.cuda.CUDAGraph()
+            with torch.cuda.graph(g):
+                if kind == "s":
+                    two.decode_step_shared(t, p, 3, prefix, lb, nb)
+                else:
+                    two.decode_step(t, p, lb, nb)
+            graphs[kind] = g
+        for step, kind in enumerate("o s s s s o s o o s o".split()):
+            t.copy_(na)
+            p += 1
+            one.decode_step(t, p, la, na)
+            graphs[kind].replay()
+            assert one.status() == mk.MK_OK and two.status() == mk.MK_OK, (step, kind)
+            a, b = la.double(), lb.double()
+            assert ((a - b).abs() <= 2e-2 + 1e-2 * a.abs()).all(), (step, kind)
+    finally:
+        one.close()
+        two.close()
+
+
 def test_shared_steps_refuse_bad_calls_and_report_bad_positions():
     hs, eng, kc, vc = engine(synth.TINY, 1, 40)
     L = mk.load()

@@ -222,6 +222,17 @@ def test_strided_tensors():
     assert (big_o[:, :, 0] == 9).all() and (big_o[:, :, 5] == 9).all()
 
 
+def test_dimensions_of_size_one_with_odd_strides():
+    c = case(1, 1, 4, 1, 64, 16, 50, [60])
+    want = attention(**c)
+    c["q"] = torch.as_strided(c["q"], c["q"].shape, (3, 5, 64, 1))
+    for x in ("k", "v"):
+        c[x] = torch.as_strided(c[x], c[x].shape, (c[x].stride(0), 7, 64, 1))
+    got, status = run(c)
+    assert status == 0
+    check_attention(got, want)
+
+
 def test_misaligned_tensors_are_refused():
     c = case(2, 1, 4, 2, 64, 16, 50, [60, 52])
     c["q"] = torch.zeros(2 * 4 * 64 + 4, device="cuda", dtype=BF16)[4:].view(2, 1, 4, 64)

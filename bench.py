@@ -78,9 +78,10 @@ def peaks():
 
 
 def src_hash() -> str:
+    """Of the sources that the decode step's kernels and plans are made from."""
     h = hashlib.sha256()
     csrc = os.path.join(ROOT, "decode_megakernel_interpreter_b200", "csrc")
-    for f in sorted(os.listdir(csrc)):
+    for f in sorted(f for f in os.listdir(csrc) if f.startswith(("interp", "mk_internal", "planner"))):
         with open(os.path.join(csrc, f), "rb") as fh:
             h.update(f.encode() + fh.read())
     return h.hexdigest()[:16]

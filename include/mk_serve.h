@@ -150,6 +150,9 @@ enum { MK_DTYPE_BF16 = 0, MK_DTYPE_F16 = 1, MK_DTYPE_F32 = 2 };
  *    influence.
  *  - A page number out of range is read as page 0, a length past the pages of
  *    its list is cut to them: MK_ERR_DEVICE_INPUT in *status.
+ *  - MK_ERR_TIMEOUT in *status: a wait inside the kernel gave up after a second
+ *    (every one is bounded); the results are then undefined.
+ *  - Results do not depend on timing: the same call gives the same bits.
  */
 typedef struct {
   int32_t batch;              /* 1 .. 1024; batch * n_tokens <= 1024 */

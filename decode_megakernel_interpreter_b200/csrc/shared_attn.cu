@@ -61,9 +61,9 @@ struct AttnDev {
   float *tagged;
   const unsigned *epoch;
   float inv_G, inv_T;
-  // the prefix on the tensor cores (tc_rows > 0; n_prefix_items is 0 then):
-  // items [kv head][group of tc_rows rows]
-  int tc_rows, tc_groups;
+  // the prefix on the tensor cores (tc_groups > 0; n_prefix_items is 0 then):
+  // items [kv head][group of kTcGroup rows]
+  int tc_groups;
   int box;         // rows of a tensor copy of K/V (0: none)
   float4 *tc_o;    // [slot][half][d / 4][kTcRows]
   float2 *tc_ml;   // [slot][half][kTcRows]
@@ -565,12 +565,13 @@ __device__ __forceinline__ void small_items(const AttnDev &p, char *sm, int *red
 //
 // S = Q K^T and O += P V as matrix instructions of 128 rows (tcgen05, operands
 // in shared memory, accumulators in tensor memory).  A block has two halves of
-// four softmax warps, a row per thread, each half with its own O, m and l:
-//   tc_rows = 256: the halves take 128 rows each and read the same K/V tiles;
-//   tc_rows = 128: both take the same rows, and every other K/V tile.
-// Each half has two S of 64 positions: the tensor cores fill one while the
-// softmax works on the other.  K/V tiles come into a ring in the order they are
-// needed, by tensor copies of the parts of a tile that lie in one page where
+// four softmax warps, a row per thread, each half with 128 rows of a group, its
+// own O, m and l, and two S of 64 positions: the tensor cores fill one while the
+// softmax works on the other.  Both halves use the same K/V tiles.  (Where a
+// group has 128 rows or less the second half is idle: giving it every other
+// tile instead measured the same or more, up to 45.7 us against 41.0, for the
+// partial results that it adds.)  K/V tiles come into a ring in the order they
+// are needed, by tensor copies of the parts of a tile that lie in one page where
 // pages are multiples of 16 positions, else by two warps 16 bytes a time, as is
 // the prefix's last tile if it is not full (that path alone kept the tensor
 // cores waiting: 42 us for 8 heads x 32768 positions x 128).  A warp for each
@@ -582,6 +583,8 @@ __device__ __forceinline__ void small_items(const AttnDev &p, char *sm, int *red
 // for an engine whose q and attention output are 32-bit numbers.
 
 constexpr int kTcRows = 128;  // rows of a half
+constexpr int kTcGroup = 2 * kTcRows;
+constexpr int kTcAhead = 2;   // K tiles that are multiplied ahead of their V
 constexpr int kTcKeys = 64;   // positions of a tile
 // warps 0-3 and 4-7: softmax; 8 and 9: copies; 10 and 11: matrix instructions.
 // (With a thirteenth warp a thread could have 128 registers only.)
@@ -745,9 +748,10 @@ __device__ __forceinline__ void cp_arrive(uint64_t *b) {
 }
 
 // The order in which the n tiles of an item pass through the ring: K of the
-// first `ahead`, then V j and K j + ahead in turn, then the other V.
+// first kTcAhead, then V j and K j + kTcAhead in turn, then the other V.
 struct TcOrder {
   int n, ahead;
+  __device__ __forceinline__ explicit TcOrder(int n_) : n(n_), ahead(min(kTcAhead, n_)) {}
   __device__ __forceinline__ int k_at(int j) const { return j < ahead ? j : 2 * j - ahead + 1; }
   __device__ __forceinline__ int v_at(int j) const { return j < n - ahead ? ahead + 2 * j : n + j; }
 };
@@ -786,11 +790,10 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   const uint32_t base = (smem_addr(sm_raw) + 1023) & ~1023u;
   char *sm = sm_raw + (base - smem_addr(sm_raw));
   const uint32_t ring = base + (kFull ? 4 : 2) * tc_q<D>();  // Q of both halves, then what it leaves
-  const bool pair = p.tc_rows == 2 * kTcRows;  // the halves have rows of their own
   if (tid == 0) {
     for (int i = 0; i < kRing; ++i) {
       bar_init(&sh.full[i], 64);
-      bar_init(&sh.empty[i], 2);  // both halves pass every entry
+      bar_init(&sh.empty[i], 2);  // both halves use every entry
     }
     for (int w = 0; w < 2; ++w) {
       bar_init(&sh.q_full[w], 4);
@@ -816,9 +819,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   __syncthreads();
   tc_after();
   const uint32_t tm = sh.tmem;
-  const int prefix = p.tc_rows ? prefix_of(p) : 0, c = blockIdx.x;
+  const int prefix = p.tc_groups ? prefix_of(p) : 0, c = blockIdx.x;
   const TcLine line(p, prefix, gridDim.x);
-  const int dist = pair ? 2 : 4;               // K tiles that are multiplied ahead of their V
   const int R = p.B * p.T * p.G;
   const bool any = c < line.share.N && line.tiles > 0;
   const int t_begin = any ? line.share.begin(c) : 0, t_end = any ? line.share.begin(c + 1) : 0;
@@ -845,7 +847,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     };
     for (int t0 = t_begin, item, first, n; ok && line.next(t0, t_end, item, first, n);) {
       const int kv = item / p.tc_groups;
-      const int ahead = min(dist, n);
+      const int ahead = min(kTcAhead, n);
       int k_next = 0, v_next = 0, k_pages = 0, v_pages = 0;
       while (v_next < n) {  // (the order of TcOrder)
         const bool is_v = k_next == n || k_next - v_next >= ahead;
@@ -909,17 +911,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     int g = 0;                          // ring entries before this item
     uint32_t q_phase = 0, p_phase = 0;  // one bit; bit i
     bool ok = true;
-    int seen = 0;                       // entries of this item taken or passed
-    // Entry e's tile has landed.  The entries before it that are the other
-    // half's are passed: waited for and let go, so that a slot's phase is never
-    // more than one ahead of, or behind, either half.
-    auto take = [&](int e) {
-      for (; ok && seen < e; ++seen) {
-        const int x = (g + seen) % kRing;
-        ok = bar_wait_all(&sh, &sh.full[x], ((g + seen) / kRing) & 1, p.status);
-        if (ok && lane == 0) bar_arrive(&sh.empty[x]);
-      }
-      seen = e + 1;
+    auto take = [&](int e) {  // entry e's tile has landed
       const int x = (g + e) % kRing;
       ok = ok && bar_wait_all(&sh, &sh.full[x], ((g + e) / kRing) & 1, p.status);
       fence_smem_async();  // the copies' writes, before the tensor cores' reads
@@ -947,19 +939,15 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         if (first == 0) p.tc_who[item].x = c;
         if (first + n == line.tiles) p.tc_who[item].y = c;
       }
-      const TcOrder order{n, min(dist, n)};
-      // this half's tiles: all (pair) or every other; its k-th S is in buffer k & 1
-      const int step = pair ? 1 : 2, j0 = pair ? 0 : w;
-      seen = 0;
-      if (item % p.tc_groups * p.tc_rows + (pair ? w * kTcRows : 0) < R && j0 < n) {  // (else the tiles only pass)
+      const TcOrder order(n);
+      if (item % p.tc_groups * kTcGroup + w * kTcRows < R) {
         ok = ok && bar_wait_all(&sh, &sh.q_full[w], q_phase, p.status);
         q_phase ^= 1;
-        for (int k = 0; ok && k < 2 && j0 + k * step < n; ++k) {
-          const int x = take(order.k_at(j0 + k * step));
-          if (ok) scores(k, x);
+        for (int j = 0; ok && j < order.ahead; ++j) {  // tile j's S is in buffer j & 1
+          const int x = take(order.k_at(j));
+          if (ok) scores(j, x);
         }
-        int i = 0;
-        for (int j = j0; ok && j < n; j += step, i ^= 1) {
+        for (int j = 0, i = 0; ok && j < n; ++j, i ^= 1) {
           const int v = take(order.v_at(j));
           ok = ok && bar_wait_all(&sh, &sh.p_full[w][i], p_phase >> i & 1, p.status);  // P is in S's place
           p_phase ^= 1u << i;
@@ -969,7 +957,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
           if (elect_one()) {
 #pragma unroll
             for (int e = 0; e < kTcKeys / 16; ++e)
-              mma_ts(o_of(w), s_of(w, i) + e * 8, tc_desc(low + e * (2048 >> 4)), kO, j > j0 || e > 0);
+              mma_ts(o_of(w), s_of(w, i) + e * 8, tc_desc(low + e * (2048 >> 4)), kO, j > 0 || e > 0);
             if (kFull)
 #pragma unroll
               for (int e = 0; e < kTcKeys / 16; ++e)
@@ -978,16 +966,16 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             mma_commit(&sh.empty[v]);
           }
           __syncwarp();
-          if (j + 2 * step < n) {
-            const int x = take(order.k_at(j + 2 * step));
+          if (j + kTcAhead < n) {
+            const int x = take(order.k_at(j + kTcAhead));
             if (ok) scores(i, x);
           }
         }
-      }
-      for (; ok && seen < 2 * n; ++seen) {
-        const int x = (g + seen) % kRing;
-        ok = bar_wait_all(&sh, &sh.full[x], ((g + seen) / kRing) & 1, p.status);
-        if (ok && lane == 0) bar_arrive(&sh.empty[x]);
+      } else {  // no rows: the tiles only pass
+        for (int e = 0; ok && e < 2 * n; ++e) {
+          const int x = take(e);
+          if (ok && lane == 0) bar_arrive(&sh.empty[x]);
+        }
       }
       g += 2 * n;
     }
@@ -1006,11 +994,9 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     bool ok = true;
     for (int t0 = t_begin, item, first, n; ok && line.next(t0, t_end, item, first, n);) {
       const int kv = item / p.tc_groups;
-      const int row = item % p.tc_groups * p.tc_rows + (pair ? w * kTcRows : 0) + r;
+      const int row = item % p.tc_groups * kTcGroup + w * kTcRows + r;
       const bool live = row < R, any_live = row - lane < R, half_live = row - r < R;
-      const int step = pair ? 1 : 2, j0 = pair ? 0 : w;
-      const bool some = half_live && j0 < n;  // this half has tiles
-      if (some) {
+      if (half_live) {
         // this row of Q (the S of the last item is done with the old one)
         const char *qp = nullptr;
         if (live) {
@@ -1044,7 +1030,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       }
       float m = -INFINITY, l = 0.f;
       int i = 0;  // which S
-      for (int j = j0; some && j < n; j += step, i ^= 1) {
+      for (int j = 0; half_live && j < n; ++j, i ^= 1) {
         ok = bar_wait_all(&sh, &sh.s_full[w][i], s_phase >> i & 1, p.status);
         s_phase ^= 1u << i;
         if (!ok) break;
@@ -1085,7 +1071,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             const float top = fmaxf(fmaxf(t[0], t[1]), fmaxf(t[2], t[3])) * p.scale2;
             const bool grow = top > (m == -INFINITY ? m : m + kGrow);
             if (!__any_sync(0xffffffffu, grow)) break;
-            if (j == j0) {
+            if (j == 0) {
               m = fmaxf(m, top);
               continue;
             }
@@ -1115,7 +1101,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         // The item's end waits for its last P V; a phase's parity only tells it
         // from the one before if that one is known to be complete, which it is
         // to be before the last P is handed over.
-        if (j + step >= n && done > 0) ok = bar_wait_all(&sh, &sh.o_full[w], (done - 1) & 1, p.status);
+        if (j + 1 == n && done > 0) ok = bar_wait_all(&sh, &sh.o_full[w], (done - 1) & 1, p.status);
         if (!ok) break;
         tc_before();
         __syncwarp();
@@ -1124,7 +1110,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       }
       if (!ok) break;
       // ---- the partial result
-      if (some) {
+      if (half_live) {
         ok = bar_wait_all(&sh, &sh.o_full[w], (done - 1) & 1, p.status);
         if (!ok) break;
         tc_after();
@@ -1133,17 +1119,14 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         const long long slot = (c + item) * 2ll + w;
         for (int q = 0; q < D / 32; ++q) {
           uint32_t x[32];
-          if (some) {
-            tm_ld32(o_of(w) + lanes + q * 32, x);
-            tm_wait_ld();
-          }
+          tm_ld32(o_of(w) + lanes + q * 32, x);
+          tm_wait_ld();
           if (live)
 #pragma unroll
             for (int i = 0; i < 8; ++i)
               p.tc_o[(slot * (D / 4) + q * 8 + i) * kTcRows + r] =
-                  some ? make_float4(__uint_as_float(x[4 * i]), __uint_as_float(x[4 * i + 1]),
-                                     __uint_as_float(x[4 * i + 2]), __uint_as_float(x[4 * i + 3]))
-                       : make_float4(0.f, 0.f, 0.f, 0.f);
+                  make_float4(__uint_as_float(x[4 * i]), __uint_as_float(x[4 * i + 1]), __uint_as_float(x[4 * i + 2]),
+                              __uint_as_float(x[4 * i + 3]));
         }
         if (live) p.tc_ml[slot * kTcRows + r] = make_float2(m, l);
       }
@@ -1187,14 +1170,12 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const AttnDev p) {
     const float4 *o1 = p.part_o, *o2 = p.part_o;
     int ms1 = kRows, rows1 = kRows;
     if (live && (how & 1)) {
-      if (p.tc_rows) {  // (a block's rows are of one group: tc_rows is a multiple of kJoinRows)
-        const int group = first / (2 * kTcRows), in = first % (2 * kTcRows) + ri, r = in % kTcRows;
-        const int item = kv * p.tc_groups + (p.tc_rows == kTcRows ? 0 : group);
+      if (p.tc_groups) {  // (a block's rows are of one half: kTcRows is a multiple of kJoinRows)
+        const int in = first % kTcGroup + ri, r = in % kTcRows, item = kv * p.tc_groups + first / kTcGroup;
         const int2 w = p.tc_who[item];
         n1 = w.y - w.x + 1;
-        const long long half = (w.x + item) * 2ll + in / kTcRows;  // pair: this row's half of each slot; else both
+        const long long half = (w.x + item) * 2ll + in / kTcRows;  // this row's half of each slot
         ms1 = 2 * kTcRows;
-        if (p.tc_rows == kTcRows) n1 *= 2, ms1 = kTcRows;
         rows1 = kTcRows;
         ml1 = p.tc_ml + half * kTcRows + r;
         o1 = p.tc_o + (half * (D / 4) + d0) * kTcRows + r;
@@ -1319,7 +1300,18 @@ int check(const mk_attn_shared_args *a) {
   return MK_OK;
 }
 
-constexpr int kTcMinRows = 17;   // rows of a K/V head from which the prefix goes to the tensor cores' kernel
+// A prefix with room for this many positions (page list x page size) is taken on
+// the tensor cores, a shorter one as items of the small kind.  Measured with 64
+// positions of a sequence's own, in us, tensor cores / small items, at 4, 64 and
+// 1024 rows a kv head:
+//   8 kv heads of 64:   512: 16.0/14.1  16.5/16.1  39.0/39.4
+//                      1024: 16.5/16.4  18.5/16.5  41.2/49.1
+//                      4096: 18.6/24.7  20.6/20.8  51.2/102.5
+//   8 kv heads of 128:  512: 17.4/14.5  19.6/18.5  47.5/48.5
+//                      1024: 18.6/18.3  20.8/20.6  51.1/62.1
+//                      4096: 20.7/34.1  23.2/29.0  63.6/139.5
+// The number of rows hardly moves the crossing.
+constexpr int kTcMinPrefix = 1024;
 
 void fill(const mk_attn_shared_args *a, AttnDev *d) {
   d->B = a->batch;
@@ -1328,9 +1320,8 @@ void fill(const mk_attn_shared_args *a, AttnDev *d) {
   d->nkv = a->n_kv_heads;
   d->G = d->nq / d->nkv;
   const int R = d->B * d->T * d->G;
-  d->tc_rows = a->n_prefix_pages > 0 && R >= kTcMinRows ? (R <= kTcRows ? kTcRows : 2 * kTcRows) : 0;
-  d->tc_groups = d->tc_rows ? (R + d->tc_rows - 1) / d->tc_rows : 0;
-  d->prefix_tiles = a->n_prefix_pages > 0 && !d->tc_rows ? (R + kRows - 1) / kRows : 0;
+  d->tc_groups = (int64_t)a->n_prefix_pages * a->page >= kTcMinPrefix ? (R + kTcGroup - 1) / kTcGroup : 0;
+  d->prefix_tiles = a->n_prefix_pages > 0 && !d->tc_groups ? (R + kRows - 1) / kRows : 0;
   d->n_prefix_items = d->nkv * d->prefix_tiles;
   d->inv_G = 1.f / (float)d->G;
   d->inv_T = 1.f / (float)d->T;
@@ -1371,7 +1362,7 @@ struct Sizes {
 };
 Sizes sizes_of(const AttnDev &d, int head_dim, int sms) {
   const int64_t rows = ((int64_t)sms * kWarps + d.n_items) * kRows;
-  const int64_t tc = d.tc_rows ? ((int64_t)sms + d.nkv * d.tc_groups) * 2 * kTcRows : 0;
+  const int64_t tc = d.tc_groups ? ((int64_t)sms + d.nkv * d.tc_groups) * 2 * kTcRows : 0;
   return Sizes{rows * head_dim * 4, rows * 8, tc * head_dim * 4, tc * 8, 8 * (int64_t)d.n_items, 8 * (int64_t)d.nkv * d.tc_groups, 4 * (int64_t)d.B};
 }
 
@@ -1463,7 +1454,7 @@ static int attn_shared(const mk_attn_shared_args *a, float *tagged, const unsign
   d.tc_who = (int2 *)part(z.tc_who);
   d.how = (int *)part(z.how);
   CUtensorMap maps[2] = {};
-  if (d.tc_rows && d.page_units) {
+  if (d.tc_groups && d.page_units) {
     const int rows = a->page % 64 == 0 ? 64 : a->page % 32 == 0 ? 32 : 16;
     if (make_map(&maps[0], a, a->k, rows) && make_map(&maps[1], a, a->v, rows)) d.box = rows;
   }

@@ -140,8 +140,9 @@ def shared_setup(shape, batch, prefix, max_seq, seed=0):
 
 
 @pytest.mark.parametrize("shape, batch, prefix", [(synth.TINY, 1, 70), (SMALL_1B, 16, 300), (SMALL_1B, 16, 0),
-                                                  (SMALL_1B, 5, 129)],
-                         ids=["tiny", "1B", "1B without a prefix", "1B batch 5"])
+                                                  (SMALL_1B, 5, 129), (synth.TINY, 1, 1100), (SMALL_1B, 16, 1300),
+                                                  (SMALL_1B, 5, 2049)],
+                         ids=["tiny", "1B", "1B without a prefix", "1B batch 5", "tiny long", "1B long", "1B batch 5 long"])
 def test_decode_over_a_shared_prefix(shape, batch, prefix):
     """Logits of shared steps against those of ordinary steps on caches that hold the prefix for every sequence; steps
     of both kinds in turn."""

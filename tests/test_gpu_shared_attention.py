@@ -51,6 +51,18 @@ def check(c, what="", scale=None):
     check_attention(got, attention(**c, scale=scale), what)
 
 
+def roomy(c, room=1100):
+    """The same call with a page list that has room for a long prefix: what lies behind the prefix is not read."""
+    n = -(-room // c["k"].shape[2])
+    old = c["prefix_pages"]
+    c["prefix_pages"] = torch.full((n,), 1 << 30, dtype=torch.int32, device="cuda")
+    if old is None:
+        c["prefix_len"] = ints([0])
+    else:
+        c["prefix_pages"][:len(old)] = old
+    return c
+
+
 HEADS = [(4, 2, 64), (8, 8, 64), (6, 2, 64), (8, 1, 128), (16, 1, 64), (4, 1, 128), (3, 3, 128)]
 
 
@@ -334,3 +346,133 @@ def test_streams_and_replayed_graphs():
             want = attention(**c)
             check_attention(o, want, "graph")
             check_attention(e, want, "stream")
+
+
+# A page list with room for a long prefix is taken by other code, whatever the prefix's length.
+
+
+@pytest.mark.parametrize("dtype", [BF16, F16])
+@pytest.mark.parametrize("nq, nkv, d", HEADS)
+def test_room_heads_and_types(nq, nkv, d, dtype):
+    check(roomy(case(3, 1, nq, nkv, d, 16, 100, [131, 100, 170], dtype)))
+
+
+@pytest.mark.parametrize("B", [1, 5, 150])
+@pytest.mark.parametrize("prefix", [0, 1, 15, 63, 64, 65, 127, 128, 129, 255, 257, 640, 1056])
+def test_room_prefix_lengths(prefix, B):
+    check(roomy(case(B, 1, 4, 2, 64, 16, prefix, [prefix + (1, 0, 63, 64, 65)[b % 5] for b in range(B)])))
+
+
+@pytest.mark.parametrize("page", [1, 3, 16, 32, 48, 64, 96, 100, 128, 1000])
+@pytest.mark.parametrize("prefix", [130, 1034])
+def test_room_page_sizes(page, prefix):
+    """Page sizes that are multiples of 16, 32 and 64 positions and that are not."""
+    check(roomy(case(4, 1, 4, 2, 128, page, prefix, [prefix + n for n in (1, 70, 65, 129)])))
+
+
+@pytest.mark.parametrize("B, T, nq", [(3, 1, 2), (3, 5, 8), (3, 16, 16), (1, 16, 16), (17, 8, 16), (130, 1, 4), (300, 2, 2)])
+def test_room_rows(B, T, nq):
+    """Rows that fill part of a group, one of its halves, both, and several groups."""
+    check(roomy(case(B, T, nq, 1, 64, 16, 70, [70 + T + 7 * b % 90 for b in range(B)], F16)))
+
+
+def test_room_sequences_shorter_than_the_prefix():
+    check(roomy(case(6, 1, 4, 2, 64, 16, 200, [200, 199, 64, 1, 0, 230])))
+    check(roomy(case(4, 4, 4, 2, 64, 16, 200, [201, 2, 0, 130])))
+    check(roomy(case(100, 4, 4, 1, 64, 16, 300, [[301, 2, 0, 130][b % 4] for b in range(100)])))
+
+
+def test_room_unused_rows_are_left_as_they_are():
+    c = roomy(case(5, 2, 4, 2, 64, 16, 100, [109, -1, 170, -(2 ** 31), 102]))
+    out = torch.full_like(c["q"], 5.0)
+    lse = torch.full((5, 2, 4), 5.0, device="cuda")
+    got, status = run(c, out=out, lse=lse)
+    assert status == 0
+    for b in (1, 3):
+        assert (out[b] == 5).all() and (lse[b] == 5).all()
+    check_attention(got, attention(**c))
+
+
+@pytest.mark.parametrize("bad", [math.nan, math.inf, -math.inf, 3e38])
+@pytest.mark.parametrize("B, page", [(3, 16), (40, 16), (40, 24)])
+def test_room_masked_positions_have_no_influence(bad, B, page):
+    prefix, lens = 90, [95 + 13 * (b % 7) if b % 5 else 41 for b in range(B)]
+    c = roomy(case(B, 1, 4, 2, 64, page, prefix, lens))
+    want = attention(**c)
+    used = torch.zeros(c["k"].shape[0], page, dtype=torch.bool)
+    for j in range(prefix):
+        used[c["prefix_pages"][j // page], j % page] = True
+    for b, n in enumerate(lens):
+        for j in range(prefix, n):
+            used[c["table"][b, j // page], j % page] = True
+    hole = (~used).cuda()[:, None, :, None]
+    for x in ("k", "v"):
+        c[x].masked_fill_(hole, bad)
+    got, status = run(c)
+    assert status == 0
+    check_attention(got, want, "unseen rows")
+
+
+@pytest.mark.parametrize("scale", [0.0, -0.2, 1.0, 1e-30])
+def test_room_scales(scale):
+    check(roomy(case(3, 2, 4, 2, 64, 16, 50, [60, 52, 120])), scale=scale)
+
+
+def test_room_bad_pages_and_lengths_are_reported():
+    base = roomy(case(3, 1, 4, 2, 64, 16, 40, [50, 45, 90]), 1040)
+    for page in (-1, base["k"].shape[0]):
+        for at in (0, 1, 2):  # a tile that is full and one that is not: in page lists of whole tiles all are read
+            c = {k: v.clone() for k, v in base.items()}
+            c["prefix_pages"][at] = page
+            assert run(c)[1] == mk.MK_ERR_DEVICE_INPUT
+    for n in (-3, 1041, 2 ** 31 - 1):
+        c = {k: v.clone() for k, v in base.items()}
+        c["prefix_pages"].clamp_(max=c["k"].shape[0] - 1)
+        c["prefix_len"][0] = n
+        assert run(c)[1] == mk.MK_ERR_DEVICE_INPUT
+    c = {k: v.clone() for k, v in base.items()}
+    c["prefix_pages"].clamp_(max=c["k"].shape[0] - 1)
+    c["prefix_pages"][20] = -1
+    c["prefix_len"][0] = 640
+    assert run(c)[1] == mk.MK_ERR_DEVICE_INPUT
+
+
+def test_room_strided_and_past_32_bits():
+    c = roomy(case(30, 1, 8, 2, 128, 64, 130, [200, 131, 333] * 10))
+    n = c["k"].shape[0]
+    want = attention(**c)
+    big = [torch.empty((300000, 2, 64, 128), dtype=BF16, device="cuda") for _ in range(2)]
+    for x, y in zip(big, (c["k"], c["v"])):
+        x[-n:] = y
+    c["k"], c["v"] = big
+    c["table"] = torch.where(c["table"] < n, c["table"] + 300000 - n, c["table"])
+    c["prefix_pages"][:3] += 300000 - n
+    got, status = run(c)
+    assert status == 0
+    check_attention(got, want)
+    del big
+    c = roomy(case(3, 2, 4, 2, 64, 16, 100, [131, 102, 170]))
+    want = attention(**c)
+    for x in ("k", "v"):  # [page][position][head] with room between rows
+        y = torch.empty((c[x].shape[0], 16, 3, 80), dtype=BF16, device="cuda")
+        y[:, :, :2, :64] = c[x].transpose(1, 2)
+        c[x] = y[:, :, :2, :64].transpose(1, 2)
+    got, status = run(c)
+    assert status == 0
+    check_attention(got, want)
+
+
+def test_room_captured_steps():
+    """A captured step replayed with prefixes and lengths of every kind."""
+    c = roomy(case(20, 1, 4, 2, 64, 16, 640, [660 + b for b in range(20)], width=48))
+    c["table"] = torch.randint(0, c["k"].shape[0], (20, 48), device="cuda", dtype=torch.int32)
+    g = torch.cuda.CUDAGraph()
+    run(c)
+    with torch.cuda.graph(g):
+        out = sv.shared_attention(**c, return_lse=True)
+    for prefix in (640, 0, 1, 64, 500, 639):
+        c["prefix_len"].fill_(prefix)
+        c["lens"].copy_(ints([prefix + 3 * b for b in range(20)]))
+        g.replay()
+        torch.cuda.synchronize()
+        check_attention(out, attention(**c), prefix)

@@ -312,9 +312,9 @@ __device__ __forceinline__ void copy_rows(const AttnDev &p, const char *k, const
 // are small (a sequence's own part, or a prefix with few rows), so what counts
 // is how many of them wait for memory at once: 12 warps an SM, each with the
 // next unit in flight.  They come before the prefix, whose partials are the
-// larger ones: the join then finds those in L2.
+// larger ones: the join then finds those in L2.  Returns the prefix's length.
 template <class T, int D, bool kFull>
-__device__ __forceinline__ void small_items(const AttnDev &p, char *sm, int *red) {
+__device__ __forceinline__ int small_items(const AttnDev &p, char *sm, int *red) {
   int *sum = reinterpret_cast<int *>(sm + smem_stages<D>());
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   constexpr int kHalf = kUnit * D * 2, kStage = 2 * kHalf;
@@ -559,6 +559,7 @@ __device__ __forceinline__ void small_items(const AttnDev &p, char *sm, int *red
         to[(d * 2 + (lane >> 1 & 1)) * kRows * 2] = make_float2(o[d][2 * h], o[d][2 * h + 1]);
     }
   }
+  return prefix;
 }
 
 // ---------------------------------------------------------------- the prefix on the tensor cores
@@ -812,15 +813,14 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_addr(&sh.tmem)) : "memory");
   pdl_wait();
   pdl_trigger();
-  small_items<T, D, kFull>(p, sm, red);
+  const int prefix = small_items<T, D, kFull>(p, sm, red), c = blockIdx.x;
   cp_wait<0>();
   fence_smem_async();  // the tensor copies reuse the small items' stages
   tc_before();
   __syncthreads();
   tc_after();
   const uint32_t tm = sh.tmem;
-  const int prefix = p.tc_groups ? prefix_of(p) : 0, c = blockIdx.x;
-  const TcLine line(p, prefix, gridDim.x);
+  const TcLine line(p, p.tc_groups ? prefix : 0, gridDim.x);
   const int R = p.B * p.T * p.G;
   const bool any = c < line.share.N && line.tiles > 0;
   const int t_begin = any ? line.share.begin(c) : 0, t_end = any ? line.share.begin(c + 1) : 0;
@@ -1146,22 +1146,33 @@ __global__ void __launch_bounds__(kTcThreads, 1)
 // all rows is contiguous: each load of a warp is 4 pieces of 128 bytes.  Of its
 // 16 warps, 4 share the elements and 4 the partials: lane q * 8 + i of warp
 // 4 s + w adds up, for row i, element groups w * D / 16 + q + 4 k of partials
-// s, s + 4, ...  The weights 2^(m - M) come first, into shared memory.
+// s, s + 4, ...  The weights 2^(m - M) come first, into shared memory, while the
+// first partials are on their way.  With kOne there is a block to each SM at
+// most, and a thread has the registers for more of them (1B, batch 16 over 8000
+// positions: 22.9 us a call against 24.8); where there are more blocks two
+// share an SM (5 drafted tokens over 5003 positions, 168 blocks: 28.7 us
+// against 30.4).
 constexpr int kJoinRows = 8;
 constexpr int kJoinThreads = 512;
 constexpr int kJoinMax = 512;  // partials of a row whose weights are kept at a time
-template <class T, int D, bool kFull>
-__global__ void __launch_bounds__(kJoinThreads) join_kernel(const AttnDev p) {
+template <class T, int D, bool kFull, bool kOne>
+__global__ void __launch_bounds__(kJoinThreads, kOne ? 1 : 2) join_kernel(const AttnDev p) {
   __shared__ float w_s[kJoinMax][kJoinRows], m_s[kJoinThreads / 32][kJoinRows], l_s[kJoinThreads / 32][kJoinRows];
   __shared__ float4 a_s[3][D / 4][kJoinRows];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, ri = lane % kJoinRows;
   const int d0 = (warp & 3) * (D / 16) + lane / kJoinRows, part = warp >> 2;
   constexpr int kGroups = D / 64;  // element groups of a lane
+  constexpr int kAhead = (kOne ? 10 : 4) / kGroups;
   pdl_wait();
   {
     const int kv = blockIdx.y, first = blockIdx.x * kJoinRows, row = min(first + ri, p.B * p.T * p.G - 1);
     // (small numbers: a half added, the product with the reciprocal is never off by one)
     const int u = (int)((row + 0.5f) * p.inv_G), b = (int)((u + 0.5f) * p.inv_T), g = row - u * p.G, t = u - b * p.T;
+    // what every part's list says is read at once; what a row has no part in is
+    // not used, whatever stands there
+    const int x = t * p.G + g, item2 = p.n_prefix_items + (b * p.nkv + kv) * p.own_tiles + x / kRows;
+    const int item1 = p.tc_groups ? kv * p.tc_groups + first / kTcGroup : kv * p.prefix_tiles + first / kRows;
+    const int2 who1 = p.tc_groups ? p.tc_who[item1] : p.n_prefix_items ? p.who[item1] : make_int2(0, -1), who2 = p.who[item2];
     const int how = p.how[b];
     const bool live = first + ri == row && how >= 0;
     // this row's partials: n1 of the prefix, n2 of its own part
@@ -1171,28 +1182,25 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const AttnDev p) {
     int ms1 = kRows, rows1 = kRows;
     if (live && (how & 1)) {
       if (p.tc_groups) {  // (a block's rows are of one half: kTcRows is a multiple of kJoinRows)
-        const int in = first % kTcGroup + ri, r = in % kTcRows, item = kv * p.tc_groups + first / kTcGroup;
-        const int2 w = p.tc_who[item];
-        n1 = w.y - w.x + 1;
-        const long long half = (w.x + item) * 2ll + in / kTcRows;  // this row's half of each slot
+        const int in = first % kTcGroup + ri, r = in % kTcRows;
+        n1 = who1.y - who1.x + 1;
+        const long long half = (who1.x + item1) * 2ll + in / kTcRows;  // this row's half of each slot
         ms1 = 2 * kTcRows;
         rows1 = kTcRows;
         ml1 = p.tc_ml + half * kTcRows + r;
         o1 = p.tc_o + (half * (D / 4) + d0) * kTcRows + r;
       } else {
-        const int item = kv * p.prefix_tiles + first / kRows, r = row % kRows;
-        const int2 w = p.who[item];
-        n1 = w.y - w.x + 1;
-        ml1 = p.part_ml + (long long)(w.x + item) * kRows + r;
-        o1 = p.part_o + ((long long)(w.x + item) * (D / 4) + d0) * kRows + r;
+        const int r = row % kRows;
+        n1 = who1.y - who1.x + 1;
+        ml1 = p.part_ml + (long long)(who1.x + item1) * kRows + r;
+        o1 = p.part_o + ((long long)(who1.x + item1) * (D / 4) + d0) * kRows + r;
       }
     }
     if (live && (how & 2)) {
-      const int x = t * p.G + g, item = p.n_prefix_items + (b * p.nkv + kv) * p.own_tiles + x / kRows, r = x % kRows;
-      const int2 w = p.who[item];
-      n2 = w.y - w.x + 1;
-      ml2 = p.part_ml + (long long)(w.x + item) * kRows + r;
-      o2 = p.part_o + ((long long)(w.x + item) * (D / 4) + d0) * kRows + r;
+      const int r = x % kRows;
+      n2 = who2.y - who2.x + 1;
+      ml2 = p.part_ml + (long long)(who2.x + item2) * kRows + r;
+      o2 = p.part_o + ((long long)(who2.x + item2) * (D / 4) + d0) * kRows + r;
     }
     // ---- the row's maximum and sum: thread 8 k + i looks at partials k, k + 64, ... of row i
     const int n = n1 + n2;
@@ -1200,9 +1208,21 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const AttnDev p) {
       const float2 *y = i < n1 ? ml1 + i * (long long)ms1 : ml2 + (i - n1) * (long long)kRows;
       return *y;
     };
-    float M = -INFINITY, L = 0.f;
+    // the first partials' elements are on their way while the weights are found
+    const float2 y0 = tid / kJoinRows < n ? ml_of(tid / kJoinRows) : make_float2(0.f, 0.f);
+    const long long step1 = (long long)ms1 * (D / 4), step2 = (long long)kRows * (D / 4);
+    o2 -= n1 * step2;
+    float4 z0[kAhead][kGroups];
+#pragma unroll
+    for (int j = 0; j < kAhead; ++j) {
+      const int i = part + 4 * j;
+#pragma unroll
+      for (int k = 0; k < kGroups; ++k)
+        if (i < n) z0[j][k] = i < n1 ? o1[i * step1 + 4 * k * rows1] : o2[i * step2 + 4 * k * kRows];
+    }
+    float M = y0.y != 0.f ? y0.x : -INFINITY, L = 0.f;
 #pragma unroll 1
-    for (int i = tid / kJoinRows; i < n; i += kJoinThreads / kJoinRows) {
+    for (int i = tid / kJoinRows + kJoinThreads / kJoinRows; i < n; i += kJoinThreads / kJoinRows) {
       const float2 y = ml_of(i);
       if (y.y != 0.f) M = fmaxf(M, y.x);
     }
@@ -1221,12 +1241,25 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const AttnDev p) {
 #pragma unroll 1
     for (int i0 = 0; i0 < n_max; i0 += kJoinMax) {
       for (int i = i0 + tid / kJoinRows; i < min(n, i0 + kJoinMax); i += kJoinThreads / kJoinRows) {
-        const float2 y = ml_of(i);
+        const float2 y = i == tid / kJoinRows ? y0 : ml_of(i);
         const float f = y.y == 0.f ? 0.f : exp2_(y.x - base);
         w_s[i - i0][ri] = f;
         L += f * y.y;
       }
       __syncthreads();
+      if (i0 == 0)
+#pragma unroll
+        for (int j = 0; j < kAhead; ++j) {
+          if (part + 4 * j >= n) break;
+          const float f = w_s[part + 4 * j][ri];
+#pragma unroll
+          for (int k = 0; k < kGroups; ++k) {
+            a[k].x = fmaf(z0[j][k].x, f, a[k].x);
+            a[k].y = fmaf(z0[j][k].y, f, a[k].y);
+            a[k].z = fmaf(z0[j][k].z, f, a[k].z);
+            a[k].w = fmaf(z0[j][k].w, f, a[k].w);
+          }
+        }
       auto add = [&](const float4 *o, long long os, int rows, int from, int to) {  // partials from, from + 4, ... of this row
 #pragma unroll 6
         for (int i = from; i < to; i += 4) {
@@ -1241,9 +1274,9 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const AttnDev p) {
           }
         }
       };
-      const int end = min(n, i0 + kJoinMax), cut = min(max(n1, i0), end), own = cut + ((part - cut) & 3);
-      add(o1, (long long)ms1 * (D / 4), rows1, i0 + part, cut);
-      add(o2 - (long long)n1 * kRows * (D / 4), (long long)kRows * (D / 4), kRows, own, end);
+      const int from = part + (i0 == 0 ? 4 * kAhead : i0), end = min(n, i0 + kJoinMax), cut = min(max(n1, i0), end);
+      add(o1, step1, rows1, from, cut);
+      add(o2, step2, kRows, max(from, cut + ((part - cut) & 3)), end);
       if (i0 + kJoinMax < n_max) __syncthreads();
     }
 #pragma unroll
@@ -1374,7 +1407,8 @@ int launch(const AttnDev &p, const CUtensorMap (&maps)[2], int sms, cudaStream_t
   if (!rc) rc = serve_launch(attn_kernel<T, D, kFull>, dim3(sms), kTcThreads, tc_smem<D, kFull>(), st, false, 1, p, maps[0], maps[1]);
   if (rc) return rc;
   const dim3 grid((p.B * p.T * p.G + kJoinRows - 1) / kJoinRows, p.nkv);
-  return serve_launch(join_kernel<T, D, kFull>, grid, kJoinThreads, 0, st, true, 1, p);
+  return grid.x * grid.y <= (unsigned)sms ? serve_launch(join_kernel<T, D, kFull, true>, grid, kJoinThreads, 0, st, true, 1, p)
+                                          : serve_launch(join_kernel<T, D, kFull, false>, grid, kJoinThreads, 0, st, true, 1, p);
 }
 
 }  // namespace

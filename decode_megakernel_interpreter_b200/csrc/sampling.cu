@@ -187,15 +187,21 @@ __global__ void __launch_bounds__(kProbThreads, kN <= 8 ? 2 : 1) probs_kernel(co
 }
 
 // The same for many rows, where registers would hold too few of them at a time:
-// a block reads its slice twice, first for the maximum and the sum, then, out
-// of L2, for the probabilities.  The slices of all blocks on the chip are about
-// 60 MB, so DRAM still sees each logit once.  (512 rows of 128256 on a B200:
-// 174 us in registers.)
+// a block takes its slice twice, first for the maximum and the sum, then for
+// the probabilities.  What it read first (16384 values) stays in shared memory,
+// the rest is read again, mostly out of L2.  Three blocks an SM, so that one
+// reads while another writes.  512 rows of 128256 on a B200: 111 us, 4.7 TB/s
+// of reads and writes, against 174 in registers; bound by the steps of a
+// cluster (read, agree, write), not by DRAM: without shared memory, when DRAM
+// saw 1.39 times the logits, it took the same, and clusters of 2 or 8 take 128.
 constexpr int kStreamThreads = 512;
 constexpr int kStreamTurns = 4;  // fours that a thread loads at a time
+constexpr int kKeptTurns = 8;    // its first ones, which stay in shared memory
+constexpr int kStreamSmem = kKeptTurns * kStreamThreads * 16;
 template <class T>
 __global__ void __launch_bounds__(kStreamThreads, 3) probs_stream_kernel(const T *logits, long long ls, const float *temperature, int ts,
                                                                          float *probs, long long ps, int vocab, int per) {
+  extern __shared__ float4 kept[];  // a thread reads what it wrote itself
   __shared__ Part part, warp_part[kStreamThreads / 32];
   cg::cluster_group cl = cg::this_cluster();
   const int C = cl.num_blocks(), rank = cl.block_rank();
@@ -230,6 +236,9 @@ __global__ void __launch_bounds__(kStreamThreads, 3) probs_stream_kernel(const T
   int first = vocab, bad = bad_t;
   for (int j0 = 0; j0 < turns; j0 += kStreamTurns) {
     load(j0, y);
+    if (j0 < kKeptTurns)
+#pragma unroll
+      for (int j = 0; j < kStreamTurns; ++j) kept[(j0 + j) * kStreamThreads + tid] = make_float4(y[j][0], y[j][1], y[j][2], y[j][3]);
     float top = -INFINITY;
 #pragma unroll
     for (int j = 0; j < kStreamTurns; ++j) top = fmaxf(top, fmaxf(fmaxf(y[j][0], y[j][1]), fmaxf(y[j][2], y[j][3])));
@@ -293,7 +302,15 @@ __global__ void __launch_bounds__(kStreamThreads, 3) probs_stream_kernel(const T
   const bool none = bad || l != l || !(m > -INFINITY && m < INFINITY);
   const float scale = none || greedy ? 0.f : 1.f / l, base = none ? 0.f : m;
   for (int j0 = 0; j0 < turns; j0 += kStreamTurns) {
-    if (!greedy && !none) load(j0, y);
+    if (j0 < kKeptTurns) {
+#pragma unroll
+      for (int j = 0; j < kStreamTurns; ++j) {
+        const float4 w = kept[(j0 + j) * kStreamThreads + tid];
+        y[j][0] = w.x, y[j][1] = w.y, y[j][2] = w.z, y[j][3] = w.w;
+      }
+    } else if (!greedy && !none) {
+      load(j0, y);
+    }
 #pragma unroll
     for (int j = 0; j < kStreamTurns; ++j) {
 #pragma unroll
@@ -516,7 +533,15 @@ template <class T>
 int launch_probs(const void *logits, int64_t ls, const float *temperature, int ts, float *probs, int64_t ps, int n, int vocab,
                  cudaStream_t st) {
   // A cluster of 8 for a large vocabulary, so that few rows still use many SMs
-  // and a slice fits into registers (up to 64 values a thread).
+  // and a slice fits into registers (up to 64 values a thread).  Below that one
+  // block is as fast (5 rows of 8192: 6.2 us with 1 and with 8).  Once there are
+  // more such blocks than two an SM (38 rows), the form for many rows, in the
+  // fewest blocks whose slices are mostly kept; in us, many / registers:
+  //   24000:  32 rows  8.3/6.5   40 rows 10.0/10.3  400 rows  18/58
+  //   128256: 32 rows 12.4/12.3  40 rows 16.4/18.6  400 rows  91/138
+  // and with 1 / 2 / 4 blocks a row, 400 rows: 16384 13.6/16.5/30.9, 24000
+  // 18.3/24.6/30.8, 32003 30.8/30.5/35.8, 50257 54.9/55.2/54.0, 128256
+  // 114/107/91 (150 rows of 32003: 18.5/16.4/16.5).
   const int C = vocab >= 16384 ? 8 : 1;
   const int per = ((vocab + C - 1) / C + 15) / 16 * 16;
   const int turns = (per + 4 * kProbThreads - 1) / (4 * kProbThreads);
@@ -526,8 +551,11 @@ int launch_probs(const void *logits, int64_t ls, const float *temperature, int t
   int sms = 0, rc = serve_sms(&sms);
   if (rc) return rc;
   if (vocab >= 16384 && (long long)n * C > 2 * sms) {
-    const int few = 4, slice = ((vocab + few - 1) / few + 15) / 16 * 16;
-    return serve_launch(probs_stream_kernel<T>, dim3((unsigned)n * few), kStreamThreads, 0, st, false, few, (const T *)logits,
+    const int few = vocab <= 24576 ? 1 : vocab <= 49152 ? 2 : 4, slice = ((vocab + few - 1) / few + 15) / 16 * 16;
+    static std::atomic<uint64_t> allowed;
+    rc = serve_allow_smem(allowed, (const void *)probs_stream_kernel<T>, kStreamSmem);
+    if (rc) return rc;
+    return serve_launch(probs_stream_kernel<T>, dim3((unsigned)n * few), kStreamThreads, kStreamSmem, st, false, few, (const T *)logits,
                         (long long)ls, temperature, ts, probs, (long long)ps, vocab, slice);
   }
   return serve_launch(fn, dim3((unsigned)n * C), kProbThreads, 0, st, false, C, (const T *)logits, (long long)ls,

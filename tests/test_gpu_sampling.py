@@ -47,7 +47,8 @@ def test_vocabularies_and_types(V, dtype):
 
 
 @pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16, torch.float16])
-@pytest.mark.parametrize("n, V", [(40, 16384), (41, 20001), (150, 32003), (75, 50004), (38, 128256)])
+@pytest.mark.parametrize("n, V", [(40, 16384), (41, 20001), (150, 32003), (75, 50004), (38, 128256), (40, 24576), (39, 24577),
+                                  (64, 49152), (38, 49153), (38, 270001)])
 def test_many_rows(n, V, dtype):
     """More rows than the chip holds at a time, with every kind of row among them."""
     g = torch.Generator(device="cuda").manual_seed(V)

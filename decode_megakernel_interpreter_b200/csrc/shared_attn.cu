@@ -1162,7 +1162,10 @@ __global__ void __launch_bounds__(kJoinThreads, kOne ? 1 : 2) join_kernel(const 
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, ri = lane % kJoinRows;
   const int d0 = (warp & 3) * (D / 16) + lane / kJoinRows, part = warp >> 2;
   constexpr int kGroups = D / 64;  // element groups of a lane
-  constexpr int kAhead = (kOne ? 10 : 4) / kGroups;
+  // partials on their way at first: as many as the registers hold (at 64 a thread
+  // and D = 128, 2 and 3 spill: 81.0 and 82.5 us against 80.0 for 64 sequences
+  // over 32768 positions)
+  constexpr int kAhead = kOne ? 10 / kGroups : D == 64 ? 4 : 1;
   pdl_wait();
   {
     const int kv = blockIdx.y, first = blockIdx.x * kJoinRows, row = min(first + ri, p.B * p.T * p.G - 1);

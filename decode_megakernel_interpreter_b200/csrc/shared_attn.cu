@@ -10,6 +10,16 @@
 // A sequence one of whose queries ends inside the prefix does not share it:
 // its whole length is then its own part, so that the shared part has no masks
 // but the prefix's end.
+//
+// One kernel of a block per SM takes the own parts, then the prefix, and a
+// second joins them.  64 sequences of 32 heads over 8 K/V heads of 128, 32768
+// positions shared and up to 1024 each of their own (270 MB, 35 GF), take
+// 80 us on a B200: own parts 28 us at 4.9 TB/s, prefix 36 us at 4 TB/s, join 9
+// us.  The prefix is bound by its memory reads and by its start behind the own
+// parts: with 7 of 8 instructions of Q K^T left out it would gain 4 us, without
+// the exponentials nothing.  Small calls are bound by the chain of dependent
+// steps (lengths, line, pages, rows, partials, join): 10.9 us with hardly any
+// data, 22.6 us for 16 sequences over 8192 positions of the 1B shape (25 MB).
 #include <cuda.h>  // CUtensorMap (types only: the encoder is looked up at run time)
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>

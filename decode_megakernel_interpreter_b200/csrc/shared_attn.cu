@@ -14,10 +14,12 @@
 // One kernel of a block per SM takes the own parts, then the prefix, and a
 // second joins them.  64 sequences of 32 heads over 8 K/V heads of 128, 32768
 // positions shared and up to 1024 each of their own (270 MB, 35 GF), take
-// 80 us on a B200: own parts 28 us at 4.9 TB/s, prefix 36 us at 4 TB/s, join 9
-// us.  The prefix is bound by its memory reads and by its start behind the own
-// parts: with 7 of 8 instructions of Q K^T left out it would gain 4 us, without
-// the exponentials nothing.  Small calls are bound by the chain of dependent
+// 78 us on a B200: own parts 28 us at 4.9 TB/s, prefix 36 us at 3.7 TB/s, join 7
+// us.  Own parts alone reach 6.6 TB/s when they are long, the prefix of 256 rows
+// 4.4 TB/s and 1110 TFLOP/s: what is lost are the starts and ends of the two
+// phases.  With 7 of 8 instructions of Q K^T left out the call would gain 4 us,
+// without the exponentials nothing; with the first prefix tiles brought into L2
+// by the warps that are done with their own parts it took 4 us more.  Small calls are bound by the chain of dependent
 // steps (lengths, line, pages, rows, partials, join): 10.9 us with hardly any
 // data, 22.6 us for 16 sequences over 8192 positions of the 1B shape (25 MB).
 #include <cuda.h>  // CUtensorMap (types only: the encoder is looked up at run time)
@@ -768,9 +770,10 @@ struct TcOrder {
 };
 
 // The blocks' line of tiles.
-// (An item's beginning and end cost a block as much as about 4 tiles: with that
-// counted, the blocks that take parts of two items end with the others.)
-constexpr int kTcItemCost = 4;
+// (An item's beginning and end cost a block as much as about 6 tiles: with that
+// counted, the blocks that take parts of two items end with the others.  256
+// rows of 8 K/V heads of 128 over 16384 positions: 44.4 us, with 4 counted 45.8.)
+constexpr int kTcItemCost = 6;
 struct TcLine {
   int tiles;
   Share share;
@@ -1173,8 +1176,8 @@ __global__ void __launch_bounds__(kJoinThreads, kOne ? 1 : 2) join_kernel(const 
   const int d0 = (warp & 3) * (D / 16) + lane / kJoinRows, part = warp >> 2;
   constexpr int kGroups = D / 64;  // element groups of a lane
   // partials on their way at first: as many as the registers hold (at 64 a thread
-  // and D = 128, 2 and 3 spill: 81.0 and 82.5 us against 80.0 for 64 sequences
-  // over 32768 positions)
+  // and D = 128, 2 and 3 spill: 1 and 2.5 of 80 us more for 64 sequences over
+  // 32768 positions)
   constexpr int kAhead = kOne ? 10 / kGroups : D == 64 ? 4 : 1;
   pdl_wait();
   {
@@ -1274,7 +1277,7 @@ __global__ void __launch_bounds__(kJoinThreads, kOne ? 1 : 2) join_kernel(const 
           }
         }
       auto add = [&](const float4 *o, long long os, int rows, int from, int to) {  // partials from, from + 4, ... of this row
-#pragma unroll 6
+#pragma unroll 4
         for (int i = from; i < to; i += 4) {
           const float f = w_s[i - i0][ri];
 #pragma unroll

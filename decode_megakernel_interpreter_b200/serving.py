@@ -37,8 +37,7 @@ def _status(t, dev):
     return None if t is None else _ints(t, 1, "status", dev)
 
 
-def _current_device() -> int:
-    return torch.cuda.current_device()
+_current_device = torch.cuda.current_device
 
 
 class _On:
@@ -238,16 +237,15 @@ def shared_attention(q, k, v, table, lens, prefix_pages=None, prefix_len=None, s
         if lse is None and return_lse:
             lse = q.new_empty((B, T, nq), dtype=torch.float32)
         os = out.stride()
-        # (a dimension of size 1 may come with any stride)
-        qs = [x if n > 1 else 8 for x, n in zip(qs, q.shape)]
-        os = [x if n > 1 else 8 for x, n in zip(os, q.shape)]
-        ks = [x if n > 1 else 8 for x, n in zip(ks, k.shape)]
         a = mk_attn_shared_args(
             B, T, nq, nkv, d, code, page, n_pages, n_prefix, table.shape[1],
             1.0 / math.sqrt(d) if scale is None else scale, q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(),
             lse.data_ptr() if lse is not None else None, pp, pl, _ints(table, 1, "table", dev),
-            _ints(lens, B, "lens", dev), _status(status, dev), qs[0], qs[1], qs[2], os[0], os[1], os[2],
-            ks[0], ks[1], ks[2])
+            _ints(lens, B, "lens", dev), None if status is None else _ints(status, 1, "status", dev),
+            # (a dimension of size 1 may come with any stride)
+            qs[0] if B > 1 else 8, qs[1] if T > 1 else 8, qs[2] if nq > 1 else 8,
+            os[0] if B > 1 else 8, os[1] if T > 1 else 8, os[2] if nq > 1 else 8,
+            ks[0] if n_pages > 1 else 8, ks[1] if nkv > 1 else 8, ks[2] if page > 1 else 8)
         L, ref = load(), ctypes.byref(a)
         n = L.mk_attn_shared_workspace_bytes(ref)
         ws = table.new_empty(max(n, 256) // 4 + 1)

@@ -6,7 +6,7 @@
 // grid-wide kernel that moves the rows the bookkeeping listed, which is
 // scheduled while the bookkeeping still runs.  The bookkeeping is bound by the
 // latency of its few dependent steps: 16 sequences resized in 11.6 us and 15
-// forked in 9.6 us, both kernels included (captured, B200).
+// forked in 10.4 us, both kernels included (captured, B200).
 #include "serve_common.h"
 
 #include <algorithm>

@@ -387,7 +387,7 @@ __device__ __forceinline__ double scan_up(double x) {  // inclusive sums over th
 // segment of kSeg values, over a block's segments, and over the cluster, always
 // in one order: the token is then found in the block, the segment and the lane
 // that the running sum passes u * sum in.  Bound by the memory latency of those
-// steps: one sequence takes 12.3 us, 64 of 128256 tokens (66 MB of rows) 23.5 us
+// steps: one sequence takes 12.3 us, 64 of 128256 tokens (66 MB of rows) 23.0 us
 // (captured, B200; blocks of 512 threads 28.9 us, clusters of 4 32.5 us, for
 // the longer slice of a block or the fewer sequences on the chip at a time).
 __global__ void __launch_bounds__(kVerThreads, 4) verify_kernel(const mk_verify_args a) {

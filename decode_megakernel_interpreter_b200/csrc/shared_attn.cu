@@ -20,8 +20,8 @@
 // phases.  With 7 of 8 instructions of Q K^T left out the call would gain 4 us,
 // without the exponentials nothing; with the first prefix tiles brought into L2
 // by the warps that are done with their own parts it took 4 us more.  Small calls are bound by the chain of dependent
-// steps (lengths, line, pages, rows, partials, join): 10.9 us with hardly any
-// data, 22.6 us for 16 sequences over 8192 positions of the 1B shape (25 MB).
+// steps (lengths, line, pages, rows, partials, join): 10.3 us with hardly any
+// data, 22.7 us for 16 sequences over 8192 positions of the 1B shape (25 MB).
 #include <cuda.h>  // CUtensorMap (types only: the encoder is looked up at run time)
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>

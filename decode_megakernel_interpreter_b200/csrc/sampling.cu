@@ -381,13 +381,22 @@ __device__ __forceinline__ double scan_up(double x) {  // inclusive sums over th
   }
   return x;
 }
+__device__ __forceinline__ double scan_max(double x) {  // largest so far over the lanes
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) x = fmax(x, __shfl_up_sync(~0u, x, o));
+  return x;
+}
 
 // A cluster per sequence.  The tokens that stand follow from single values;
 // the new token from one row of p (and q), whose 64-bit sums are taken per
 // segment of kSeg values, over a block's segments, and over the cluster, always
 // in one order: the token is then found in the block, the segment and the lane
-// that the running sum passes u * sum in.  Bound by the memory latency of those
-// steps: one sequence takes 12.3 us, 64 of 128256 tokens (66 MB of rows) 23.0 us
+// that the running sum passes u * sum in.  The lanes' sums add the same values
+// up in different orders, so a running sum could come out below the one before
+// it, or above it where nothing was added: each is therefore the largest so far,
+// a segment of weight 0 keeps the last one's, and the last one is the block's
+// sum for all.  The blocks' ranges then meet without gaps, and a segment that
+// passes the goal holds a weight.  Bound by the memory latency of those steps: one sequence takes 12.3 us, 64 of 128256 tokens (66 MB of rows) 23.0 us
 // (captured, B200; blocks of 512 threads 28.9 us, clusters of 4 32.5 us, for
 // the longer slice of a block or the fewer sequences on the chip at a time).
 __global__ void __launch_bounds__(kVerThreads, 4) verify_kernel(const mk_verify_args a) {
@@ -455,9 +464,10 @@ __global__ void __launch_bounds__(kVerThreads, 4) verify_kernel(const mk_verify_
     if (warp == 0) {
       double run = 0.0;
       for (int s = 0; s < s1 - s0; s += 32) {
-        const double x = run + scan_up(s + lane < s1 - s0 ? seg[s + lane] : 0.0);
+        const double own = s + lane < s1 - s0 ? seg[s + lane] : 0.0, up_to = run + scan_up(own);
+        const double x = scan_max(own > 0.0 ? up_to : run);
         if (s + lane < s1 - s0) seg[s + lane] = x;
-        run = __shfl_sync(~0u, x, 31);
+        run = __shfl_sync(~0u, x, 31);  // (that of the last segment, where there are fewer)
       }
       if (lane == 0) total = run;
     }

@@ -45,7 +45,9 @@ constexpr int kItemCost = 2;
 constexpr int kMaxRowsB = 1024;
 // A row's maximum only moves when it grows by more than 2^8: until then the
 // weights are at most 2^8, which neither type nor the 32-bit sums mind, and the
-// sums so far need not be rescaled.
+// sums so far need not be rescaled.  fp16 has room above that and little below
+// (what is less than 2^-25 becomes 0, which many positions of small weight would
+// miss): its weights are taken in units of 2^-kShift of the maximum.
 constexpr float kGrow = 8.f;
 
 struct AttnDev {
@@ -209,6 +211,7 @@ template <class T>
 struct Num;
 template <>
 struct Num<__nv_bfloat16> {
+  static constexpr float kShift = 0.f;
   static __device__ __forceinline__ void mma(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
     asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
                  : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
@@ -227,6 +230,7 @@ struct Num<__nv_bfloat16> {
 };
 template <>
 struct Num<__half> {
+  static constexpr float kShift = 7.f;  // 2^(kGrow + kShift) is below the type's largest
   static __device__ __forceinline__ void mma(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
     asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
                  : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
@@ -496,7 +500,7 @@ __device__ __forceinline__ int small_items(const AttnDev &p, char *sm, int *red)
       }
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        const float base = m[h] == -INFINITY ? 0.f : m[h];
+        const float base = m[h] == -INFINITY ? 0.f : m[h] - Num<T>::kShift;
         float t = 0.f;
 #pragma unroll
         for (int n = 0; n < 2; ++n)
@@ -564,7 +568,7 @@ __device__ __forceinline__ int small_items(const AttnDev &p, char *sm, int *red)
       l[h] += __shfl_xor_sync(0xffffffffu, l[h], 1);
       l[h] += __shfl_xor_sync(0xffffffffu, l[h], 2);
       if (r >= n_rows) continue;
-      if ((lane & 3) == 0) p.part_ml[(long long)slot * kRows + r] = make_float2(m[h], l[h]);
+      if ((lane & 3) == 0) p.part_ml[(long long)slot * kRows + r] = make_float2(m[h] - Num<T>::kShift, l[h]);
       float2 *to = reinterpret_cast<float2 *>(p.part_o + (long long)slot * (D / 4) * kRows + r) + (lane & 1);
 #pragma unroll
       for (int d = 0; d < D / 8; ++d)
@@ -1066,7 +1070,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
           uint32_t h[32], g[kFull ? 32 : 1];
           unsigned long long sum;
           for (;;) {
-            const float b = m == -INFINITY ? 0.f : m;
+            const float b = m == -INFINITY ? 0.f : m - Num<T>::kShift;
             const unsigned long long scale = pack2(p.scale2, p.scale2), minus = pack2(-b, -b);
             float t[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
             sum = 0ull;
@@ -1141,7 +1145,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                   make_float4(__uint_as_float(x[4 * i]), __uint_as_float(x[4 * i + 1]), __uint_as_float(x[4 * i + 2]),
                               __uint_as_float(x[4 * i + 3]));
         }
-        if (live) p.tc_ml[slot * kTcRows + r] = make_float2(m, l);
+        if (live) p.tc_ml[slot * kTcRows + r] = make_float2(m - Num<T>::kShift, l);
       }
       tc_before();
     }

@@ -24,6 +24,19 @@ __device__ __forceinline__ float up(__half x) { return __half2float(x); }
 
 constexpr int kProbThreads = 512;
 
+// The factor log2(e) / T.  For T below kTinyT (`tiny`) it passes 32 bits, and is
+// taken as 2^64 times a smaller one.  Where values are in registers every row has
+// both multiplications (5 rows of 128256 take the same); the form for many rows,
+// which they cost 2 % (512 rows 113 us, not 111), has a body for tiny T.
+constexpr float kTinyT = 1e-37f;
+struct PerT {
+  float a, f;
+  __device__ __forceinline__ PerT(float t, bool tiny)
+      : a(tiny ? 0x1p64f : 1.f), f((float)(1.4426950408889634 / ((double)t * (double)a))) {}
+  // x / T in powers of two
+  __device__ __forceinline__ float operator()(float x) const { return x * a * f; }
+};
+
 // A block's part of a row, for the others of the cluster.
 struct Part {
   float m, l;  // largest logit of the slice; sum of exp((z - m) / T)
@@ -124,10 +137,11 @@ __global__ void __launch_bounds__(kProbThreads, kN <= 8 ? 2 : 1) probs_kernel(co
 
   // ---- sum of exp((z - m) / T), in powers of two (32-bit: the logit's
   // difference, log2(e) / T and their product are each rounded once)
-  const float c = greedy || bad ? 0.f : (float)(1.4426950408889634 / (double)t), base = m == -INFINITY ? 0.f : m;
+  const PerT c(greedy || bad ? 1.f : t, !greedy && t < kTinyT);
+  const float base = m == -INFINITY ? 0.f : m;
   auto ex = [&](float y) {
     float r;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"((y - base) * c));
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(c(y - base)));
     return r;
   };
   float l = 0.f;
@@ -161,7 +175,7 @@ __global__ void __launch_bounds__(kProbThreads, kN <= 8 ? 2 : 1) probs_kernel(co
     bad |= warp_part[r].bad;
   }
   const float Mb = M == -INFINITY ? 0.f : M;
-  auto to_row = [&](float y) { return exp2f((y - Mb) * c); };  // exp((y - M) / T), for a slice's largest logit y
+  auto to_row = [&](float y) { return exp2f(c(y - Mb)); };  // exp((y - M) / T), for a slice's largest logit y
   if (!greedy)
     for (int r = 0; r < C; ++r) L += warp_part[r].l * to_row(warp_part[r].m);
   // (a NaN among the logits shows in the sum)
@@ -198,9 +212,9 @@ constexpr int kStreamThreads = 512;
 constexpr int kStreamTurns = 4;  // fours that a thread loads at a time
 constexpr int kKeptTurns = 8;    // its first ones, which stay in shared memory
 constexpr int kStreamSmem = kKeptTurns * kStreamThreads * 16;
-template <class T>
-__global__ void __launch_bounds__(kStreamThreads, 3) probs_stream_kernel(const T *logits, long long ls, const float *temperature, int ts,
-                                                                         float *probs, long long ps, int vocab, int per) {
+template <class T, bool kTiny>
+__device__ __forceinline__ void probs_stream_row(const T *logits, long long ls, const float t, float *probs, long long ps, int vocab,
+                                                 int per) {
   extern __shared__ float4 kept[];  // a thread reads what it wrote itself
   __shared__ Part part, warp_part[kStreamThreads / 32];
   cg::cluster_group cl = cg::this_cluster();
@@ -209,10 +223,9 @@ __global__ void __launch_bounds__(kStreamThreads, 3) probs_stream_kernel(const T
   const int v0 = min(rank * per, vocab), n = min(per, vocab - v0);
   const T *z = logits + row * ls + v0;
   float *out = probs + row * ps + v0;
-  const float t = temperature ? temperature[row * ts] : 1.f;
   const bool greedy = t == 0.f;
   const int bad_t = !(t >= 0.f && t < INFINITY);
-  const float c = greedy || bad_t ? 0.f : (float)(1.4426950408889634 / (double)t);
+  const PerT c(greedy || bad_t ? 1.f : t, kTiny);
   const bool vec = (reinterpret_cast<uintptr_t>(z) & (4 * sizeof(T) - 1)) == 0 && (reinterpret_cast<uintptr_t>(out) & 15) == 0;
   auto at = [&](int j, int e) { return j * 4 * kStreamThreads + (vec ? tid * 4 + e : e * kStreamThreads + tid); };
   const int turns = (n + 4 * kStreamThreads - 1) / (4 * kStreamThreads);
@@ -229,7 +242,7 @@ __global__ void __launch_bounds__(kStreamThreads, 3) probs_stream_kernel(const T
   };
   auto ex = [&](float y, float base) {
     float r;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"((y - base) * c));
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(c(y - base)));
     return r;
   };
   float m = -INFINITY, l = 0.f, y[kStreamTurns][4];
@@ -326,6 +339,15 @@ __global__ void __launch_bounds__(kStreamThreads, 3) probs_stream_kernel(const T
     }
   }
   cl.barrier_wait();
+}
+
+template <class T>
+__global__ void __launch_bounds__(kStreamThreads, 3) probs_stream_kernel(const T *logits, long long ls, const float *temperature, int ts,
+                                                                         float *probs, long long ps, int vocab, int per) {
+  const int row = blockIdx.x / cg::this_cluster().num_blocks();
+  const float t = temperature ? temperature[row * ts] : 1.f;
+  if (t > 0.f && t < kTinyT) probs_stream_row<T, true>(logits, ls, t, probs, ps, vocab, per);
+  else probs_stream_row<T, false>(logits, ls, t, probs, ps, vocab, per);
 }
 
 // ---------------------------------------------------------------- verification

@@ -171,13 +171,17 @@ __global__ void __launch_bounds__(kMetaThreads) resize_kernel(State s, const int
     for (int j = 0; j < i; ++j) before += last_s[j] == last;
     cow = refs - before > 1;
   }
-  int need = grows ? ceil_div(want, page) - b + cow : 0, total;
+  // new pages of this entry; more than there are is as good as one more, and
+  // kMaxList of them then add up in 32 bits
+  const int more = grows ? min(ceil_div(want, page) - b, s.n_pages + 1) : 0;
+  static_assert((long long)kMaxList * (kMaxPages + 2) < 1ll << 31, "sums of needed pages");
+  int need = more + cow, total;
   int start = block_incl_sum(need, red, &total) - need;
   bool take = grows;
   if (total > top) {
     // Not enough pages: decide entry by entry, as the list is ordered.  A
     // skipped entry does not copy, so the next holder's turn changes with it.
-    start_s[i] = grows ? ceil_div(want, page) - b : -1;
+    start_s[i] = grows ? more : -1;
     __syncthreads();
     if (i == 0) {
       int used = 0;

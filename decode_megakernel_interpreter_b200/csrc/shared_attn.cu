@@ -42,6 +42,11 @@ constexpr int kStages = 2;   // units of a warp in shared memory
 // What beginning and ending an item costs a warp, in units (about 3.5 us against
 // 1.9): without it the warps with many short items were the last by 15 us.
 constexpr int kItemCost = 2;
+// The matrix instructions cut what they add to a sum off below its last bit, so
+// a long sum comes out low: by 4e-9 of itself for each position (2^18 in one sum:
+// 1.2e-3, more than a step of fp16).  A part longer than this many positions is
+// therefore taken in several, which are added up with the partial so far.
+constexpr int kMaxSum = 16384;
 constexpr int kMaxRowsB = 1024;
 // A row's maximum only moves when it grows by more than 2^8: until then the
 // weights are at most 2^8, which neither type nor the 32-bit sums mind, and the
@@ -248,6 +253,19 @@ struct Num<__half> {
   }
 };
 
+// Add a row's partial (m, l) to the one so far; then its elements.
+struct Sum {
+  float now, before;  // factors
+  __device__ __forceinline__ Sum(float &m, float &l, float2 so_far) {
+    const float M = fmaxf(m, so_far.x), base = M == -INFINITY ? 0.f : M;
+    now = exp2_(m - base);
+    before = exp2_(so_far.x - base);
+    m = M;
+    l = l * now + so_far.y * before;
+  }
+  __device__ __forceinline__ float operator()(float x, float y) const { return fmaf(y, before, x * now); }
+};
+
 // Two numbers as the type's nearest, and what that leaves as another.
 template <class T>
 __device__ __forceinline__ void two_parts(float2 x, uint32_t &hi, uint32_t &lo) {
@@ -341,6 +359,7 @@ __device__ __forceinline__ int small_items(const AttnDev &p, char *sm, int *red)
   const int c = warp * gridDim.x + blockIdx.x;  // (neighbours along the line on different SMs)
   int t0 = c < line.share.N && line.share.total > 0 ? line.share.begin(c) : 0;
   const int t_end = c < line.share.N && line.share.total > 0 ? line.share.begin(c + 1) : 0;
+  int last_item = -1;
 
   while (t0 < t_end) {
     // ---- which item, and which of its units
@@ -376,9 +395,11 @@ __device__ __forceinline__ int small_items(const AttnDev &p, char *sm, int *red)
       lo = shares(p, hi, prefix) ? prefix : 0;
     }
     const int item_end = item_t0 + item_n, begin = max(t0, item_t0 + kItemCost), first = begin - item_t0 - kItemCost;
-    const int n = min(t_end, item_end) - begin;
-    t0 = min(t_end, item_end);
+    const int n = min(min(t_end, item_end) - begin, kMaxSum / kUnit);
+    t0 = n > 0 ? begin + n : min(t_end, item_end);
     if (n <= 0) continue;  // (the item's cost alone)
+    const bool again = item == last_item;
+    last_item = item;
     if (lane == 0) {
       if (first == 0) p.who[item].x = c;
       if (t0 == item_end) p.who[item].y = c;
@@ -567,8 +588,23 @@ __device__ __forceinline__ int small_items(const AttnDev &p, char *sm, int *red)
       const int r = lane / 4 + 8 * h;
       l[h] += __shfl_xor_sync(0xffffffffu, l[h], 1);
       l[h] += __shfl_xor_sync(0xffffffffu, l[h], 2);
+      m[h] -= Num<T>::kShift;
+      float2 *const ml = p.part_ml + (long long)slot * kRows + r;
+      if (again) {  // (the same lanes wrote it)
+        const Sum sum(m[h], l[h], r < n_rows ? *ml : make_float2(-INFINITY, 0.f));
+        if (r < n_rows) {
+          const float2 *from = reinterpret_cast<float2 *>(p.part_o + (long long)slot * (D / 4) * kRows + r) + (lane & 1);
+#pragma unroll
+          for (int d = 0; d < D / 8; ++d) {
+            const float2 y = from[(d * 2 + (lane >> 1 & 1)) * kRows * 2];
+            o[d][2 * h] = sum(o[d][2 * h], y.x);
+            o[d][2 * h + 1] = sum(o[d][2 * h + 1], y.y);
+          }
+        }
+        __syncwarp();  // ml is read
+      }
       if (r >= n_rows) continue;
-      if ((lane & 3) == 0) p.part_ml[(long long)slot * kRows + r] = make_float2(m[h] - Num<T>::kShift, l[h]);
+      if ((lane & 3) == 0) *ml = make_float2(m[h], l[h]);
       float2 *to = reinterpret_cast<float2 *>(p.part_o + (long long)slot * (D / 4) * kRows + r) + (lane & 1);
 #pragma unroll
       for (int d = 0; d < D / 8; ++d)
@@ -783,21 +819,23 @@ struct TcLine {
   Share share;
   __device__ __forceinline__ TcLine(const AttnDev &p, int prefix, int blocks)
       : tiles((prefix + kTcKeys - 1) / kTcKeys), share(tiles > 0 ? (tiles + kTcItemCost) * p.nkv * p.tc_groups : 0, blocks) {}
-  // The next part of a block's share [t0, t_end): false when there is none.
+  // The next part of a block's share [t0, t_end), with kLong kMaxSum positions at most: false when there is none.
+  template <bool kLong>
   __device__ __forceinline__ bool next(int &t0, int t_end, int &item, int &first, int &n) const {
     while (t0 < t_end) {
       item = t0 / (tiles + kTcItemCost);
       const int at = item * (tiles + kTcItemCost), end = min(t_end, at + tiles + kTcItemCost), from = max(t0, at + kTcItemCost);
-      t0 = end;
       first = from - at - kTcItemCost;
-      n = end - from;
+      n = kLong ? min(end - from, kMaxSum / kTcKeys) : end - from;
+      t0 = n > 0 ? from + n : end;
       if (n > 0) return true;
     }
     return false;
   }
 };
 
-template <class T, int D, bool kFull>
+// kLong: a block's share of the prefix may be longer than kMaxSum.
+template <class T, int D, bool kFull, bool kLong>
 __global__ void __launch_bounds__(kTcThreads, 1)
     attn_kernel(const AttnDev p, const __grid_constant__ CUtensorMap k_map, const __grid_constant__ CUtensorMap v_map) {
   extern __shared__ char sm_raw[];
@@ -862,7 +900,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         phase ^= 1;
       }
     };
-    for (int t0 = t_begin, item, first, n; ok && line.next(t0, t_end, item, first, n);) {
+    for (int t0 = t_begin, item, first, n; ok && line.next<kLong>(t0, t_end, item, first, n);) {
       const int kv = item / p.tc_groups;
       const int ahead = min(kTcAhead, n);
       int k_next = 0, v_next = 0, k_pages = 0, v_pages = 0;
@@ -951,7 +989,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       }
       __syncwarp();
     };
-    for (int t0 = t_begin, item, first, n; ok && line.next(t0, t_end, item, first, n);) {
+    for (int t0 = t_begin, item, first, n; ok && line.next<kLong>(t0, t_end, item, first, n);) {
       if (w == 0 && lane == 0) {
         if (first == 0) p.tc_who[item].x = c;
         if (first + n == line.tiles) p.tc_who[item].y = c;
@@ -1008,8 +1046,9 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     const uint32_t lanes = (uint32_t)(warp & 3) << 21;  // this warp's 32 lanes of tensor memory
     uint32_t s_phase = 0;  // bit i
     int done = 0;          // tiles of this half so far
+    int last_item = -1;
     bool ok = true;
-    for (int t0 = t_begin, item, first, n; ok && line.next(t0, t_end, item, first, n);) {
+    for (int t0 = t_begin, item, first, n; ok && line.next<kLong>(t0, t_end, item, first, n);) {
       const int kv = item / p.tc_groups;
       const int row = item % p.tc_groups * kTcGroup + w * kTcRows + r;
       const bool live = row < R, any_live = row - lane < R, half_live = row - r < R;
@@ -1134,19 +1173,32 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       }
       if (any_live) {
         const long long slot = (c + item) * 2ll + w;
+        const bool again = kLong && live && item == last_item;
+        m -= Num<T>::kShift;
+        const Sum sum(m, l, again ? p.tc_ml[slot * kTcRows + r] : make_float2(-INFINITY, 0.f));
         for (int q = 0; q < D / 32; ++q) {
           uint32_t x[32];
           tm_ld32(o_of(w) + lanes + q * 32, x);
           tm_wait_ld();
+          float4 *const to = p.tc_o + (slot * (D / 4) + q * 8) * kTcRows + r;
+          if (again)
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              const float4 y = to[i * kTcRows];
+              x[4 * i] = __float_as_uint(sum(__uint_as_float(x[4 * i]), y.x));
+              x[4 * i + 1] = __float_as_uint(sum(__uint_as_float(x[4 * i + 1]), y.y));
+              x[4 * i + 2] = __float_as_uint(sum(__uint_as_float(x[4 * i + 2]), y.z));
+              x[4 * i + 3] = __float_as_uint(sum(__uint_as_float(x[4 * i + 3]), y.w));
+            }
           if (live)
 #pragma unroll
             for (int i = 0; i < 8; ++i)
-              p.tc_o[(slot * (D / 4) + q * 8 + i) * kTcRows + r] =
-                  make_float4(__uint_as_float(x[4 * i]), __uint_as_float(x[4 * i + 1]), __uint_as_float(x[4 * i + 2]),
-                              __uint_as_float(x[4 * i + 3]));
+              to[i * kTcRows] = make_float4(__uint_as_float(x[4 * i]), __uint_as_float(x[4 * i + 1]), __uint_as_float(x[4 * i + 2]),
+                                            __uint_as_float(x[4 * i + 3]));
         }
-        if (live) p.tc_ml[slot * kTcRows + r] = make_float2(m - Num<T>::kShift, l);
+        if (live) p.tc_ml[slot * kTcRows + r] = make_float2(m, l);
       }
+      last_item = item;
       tc_before();
     }
   }
@@ -1419,12 +1471,22 @@ Sizes sizes_of(const AttnDev &d, int head_dim, int sms) {
   return Sizes{rows * head_dim * 4, rows * 8, tc * head_dim * 4, tc * 8, 8 * (int64_t)d.n_items, 8 * (int64_t)d.nkv * d.tc_groups, 4 * (int64_t)d.B};
 }
 
-template <class T, int D, bool kFull = false>
-int launch(const AttnDev &p, const CUtensorMap (&maps)[2], int sms, cudaStream_t st) {
+template <class T, int D, bool kFull, bool kLong>
+int launch_attn(const AttnDev &p, const CUtensorMap (&maps)[2], int sms, cudaStream_t st) {
   static_assert(smem_stages<D>() + 4 * (kMaxRowsB + 1) + 1024 <= tc_smem<D, kFull>(), "the small items' stages and sums fit");
   static std::atomic<uint64_t> allowed;
-  int rc = serve_allow_smem(allowed, (const void *)attn_kernel<T, D, kFull>, tc_smem<D, kFull>());
-  if (!rc) rc = serve_launch(attn_kernel<T, D, kFull>, dim3(sms), kTcThreads, tc_smem<D, kFull>(), st, false, 1, p, maps[0], maps[1]);
+  const int rc = serve_allow_smem(allowed, (const void *)attn_kernel<T, D, kFull, kLong>, tc_smem<D, kFull>());
+  return rc ? rc : serve_launch(attn_kernel<T, D, kFull, kLong>, dim3(sms), kTcThreads, tc_smem<D, kFull>(), st, false, 1, p, maps[0], maps[1]);
+}
+
+template <class T, int D, bool kFull = false>
+int launch(const AttnDev &p, const CUtensorMap (&maps)[2], int sms, cudaStream_t st) {
+  // Where a page list has no room for more than kMaxSum positions a block, the
+  // kernel is built without the adding up (which costs the softmax warps
+  // registers: 64 sequences over 32768 positions 79.3 us with it, 76.0 without).
+  const int64_t tiles = (int64_t)p.n_prefix_pages * p.page / kTcKeys + 1 + kTcItemCost;
+  const bool is_long = tiles * p.nkv * p.tc_groups / sms + 1 > kMaxSum / kTcKeys;
+  int rc = is_long ? launch_attn<T, D, kFull, true>(p, maps, sms, st) : launch_attn<T, D, kFull, false>(p, maps, sms, st);
   if (rc) return rc;
   const dim3 grid((p.B * p.T * p.G + kJoinRows - 1) / kJoinRows, p.nkv);
   return grid.x * grid.y <= (unsigned)sms ? serve_launch(join_kernel<T, D, kFull, true>, grid, kJoinThreads, 0, st, true, 1, p)

@@ -913,8 +913,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         if (p.box && pos0 + kTcKeys <= prefix) {
           int pages = is_v ? v_pages : k_pages;
           if ((j & tiles_mask) == 0) {
-            const int pos = pos0 + lane * p.box;
-            pages = pos < prefix ? p.prefix_pages[page_index(p, pos)] : 0;
+            const unsigned pos = (unsigned)pos0 + lane * p.box;  // (up to 31 boxes past a prefix that ends just below 2^31)
+            pages = pos < (unsigned)prefix ? p.prefix_pages[page_index(p, (int)pos)] : 0;
             if (is_v) v_pages = pages;
             else k_pages = pages;
           }

@@ -759,6 +759,7 @@ struct TcShared {
   uint64_t full[16], empty[16];  // ring entries
   uint64_t q_full[2], s_full[2][2], p_full[2][2], o_full[2], drain[2];  // [half][which S]; o_full: a P V is complete
   uint32_t tmem;
+  int sent[2];        // tiles that each copying warp has arrived for
   volatile int dead;  // a wait gave up
 };
 
@@ -787,6 +788,11 @@ __device__ __forceinline__ bool bar_wait_all(TcShared *sh, uint64_t *b, uint32_t
 }
 __device__ __forceinline__ void bar_expect(uint64_t *b, uint32_t bytes) {
   asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(smem_addr(b)), "r"(bytes) : "memory");
+}
+// Wait for a phase until the clock says `end`.
+__device__ __forceinline__ void bar_wait_until(uint64_t *b, uint32_t parity, uint64_t end) {
+  uint64_t t = 0;
+  while (!bar_try(b, parity) && t < end) asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t));
 }
 // A box of K or V: 64 elements from x on, of the map's number of rows.
 __device__ __forceinline__ void tensor_copy(const CUtensorMap *map, uint32_t dst, int x, int row, int kv, int page, uint64_t *b) {
@@ -885,7 +891,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   if (warp >= 8 && warp < 10) {
     // ---------------- copies: warp w of the two takes rows 32 w .. 32 w + 31
     // of every tile, 16 at a time
-    int slot = 0;         // of the ring
+    int slot = 0, sent = 0;  // of the ring; tiles so far
     uint32_t phase = 1;   // of its `empty`: every slot is free at first
     bool ok = true;
     const int row = (warp - 8) * 32, ch = lane % (D / 8), r0 = lane / (D / 8);
@@ -895,6 +901,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     const int box_row = (lane & (boxes - 1)) * p.box;
     const uint32_t box_at = box_row * 128;
     auto step = [&]() {
+      ++sent;
       if (++slot == kRing) {
         slot = 0;
         phase ^= 1;
@@ -952,6 +959,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     }
     cp_commit();
     cp_wait<0>();
+    if (lane == 0) sh.sent[warp - 8] = sent;
   } else if (warp >= 10) {
     // ---------------- matrix instructions of half w: the warp walks as one, an
     // elected lane issues
@@ -1033,12 +1041,6 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         }
       }
       g += 2 * n;
-    }
-    if (!ok) {  // given up: the instructions in flight end before tensor memory goes
-      if (elect_one()) mma_commit(&sh.drain[w]);
-      __syncwarp();
-      for (int i = 0; i < 100000 && !__all_sync(0xffffffffu, bar_try(&sh.drain[w], 0)); ++i) {
-      }
     }
   } else if (warp < 8) {
     // ---------------- softmax: row r of half w
@@ -1203,6 +1205,26 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     }
   }
   __syncthreads();
+  if (sh.dead) {
+    // Given up: what is in flight ends before shared and tensor memory go, within
+    // a second.  The matrix instructions of both halves, whichever role gave up:
+    uint64_t end;
+    asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(end));
+    end += 1000000000ull;
+    if (warp >= 10) {
+      if (elect_one()) mma_commit(&sh.drain[warp - 10]);
+      __syncwarp();
+      bar_wait_until(&sh.drain[warp - 10], 0, end);
+    }
+    // The tensor copies: an entry's phase ends with them once both copying warps
+    // have arrived, so the arrivals of the one that is behind are made up for.
+    if (warp == 8) {
+      const int a = min(sh.sent[0], sh.sent[1]), b = max(sh.sent[0], sh.sent[1]);
+      for (int e = a; e < b; ++e) bar_arrive(&sh.full[e % kRing]);
+      for (int e = max(0, b - kRing); e < b; ++e) bar_wait_until(&sh.full[e % kRing], e / kRing & 1, end);
+    }
+    __syncthreads();
+  }
   if (warp == 10) {
     tc_after();
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");

@@ -7,7 +7,8 @@ is asynchronous on the current stream of its tensors' device (or on `stream`),
 takes its scratch from torch's allocator on that stream, and can be captured
 into a CUDA graph.  Tensors of one call are on one device, which need not be
 the current one.  Arguments that do not fit raise ValueError, codes of the
-library MkError.
+library MkError.  An empty list or batch is a call without work: it returns its
+(empty) outputs and launches nothing.
 """
 from __future__ import annotations
 
@@ -153,6 +154,8 @@ def _kv_call(pool: KvPool, state: KvState, n: int, stream, what: str, call) -> N
     _need(pool.device == state.device and pool.n_pages == state.n_pages,
           "the state is another pool's (device or number of pages)")
     with _On(pool.device, stream) as s:
+        if n == 0:
+            return
         ws = torch.empty(load().mk_kv_workspace_bytes(pool.n_pages, n), dtype=torch.uint8, device=pool.device)
         _check(call(ws.data_ptr(), s), what)
 
@@ -190,6 +193,8 @@ def kv_copy(src: KvPool, dst: KvPool, items, status=None, stream=None) -> None:
     n = items.shape[0]
     p = _ints(items, 5 * n, "items", src.device)
     with _On(src.device, stream) as s:
+        if n == 0:
+            return
         L = load()
         ws = torch.empty(L.mk_kv_workspace_bytes(1, n), dtype=torch.uint8, device=src.device)
         _check(L.mk_kv_copy(src._ref, dst._ref, p, n, _status(status, src.device), ws.data_ptr(), s), "mk_kv_copy")
@@ -236,6 +241,8 @@ def shared_attention(q, k, v, table, lens, prefix_pages=None, prefix_len=None, s
             out = q.new_empty((B, T, nq, d))
         if lse is None and return_lse:
             lse = q.new_empty((B, T, nq), dtype=torch.float32)
+        if B == 0:
+            return (out, lse) if return_lse else out
         os = out.stride()
         a = mk_attn_shared_args(
             B, T, nq, nkv, d, code, page, n_pages, n_prefix, table.shape[1],
@@ -272,6 +279,8 @@ def token_probs(logits, temperature=None, out=None, stream=None):
         else:
             _need(out.shape == logits.shape and out.dtype is torch.float32 and out.stride(1) == 1 and out.device == dev,
                   "out: float [rows][vocab], rows contiguous")
+        if n == 0:
+            return out
         _check(load().mk_token_probs(logits.data_ptr(), DTYPES[logits.dtype], logits.stride(0), t, out.data_ptr(),
                                      out.stride(0), n, V, s), "mk_token_probs")
     return out
@@ -300,6 +309,8 @@ def verify(target, draft, tokens, u, n_drafted=None, status=None, stream=None):
     with _On(dev, stream) as s:
         out = torch.empty((B, T + 1), dtype=torch.int32, device=dev)
         acc = torch.empty(B, dtype=torch.int32, device=dev)
+        if B == 0:
+            return out, acc
         ts = target.stride()
         a = mk_verify_args(B, T, V, target.data_ptr(), d, x, n, u.data_ptr(), out.data_ptr(), acc.data_ptr(),
                            _status(status, dev), ts[0], ts[1], ds[0], ds[1])

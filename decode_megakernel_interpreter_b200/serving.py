@@ -8,7 +8,8 @@ takes its scratch from torch's allocator on that stream, and can be captured
 into a CUDA graph.  Tensors of one call are on one device, which need not be
 the current one.  Arguments that do not fit raise ValueError, codes of the
 library MkError.  An empty list or batch is a call without work: it returns its
-(empty) outputs and launches nothing.
+(empty) outputs and launches nothing.  There are no backward passes: tensors
+that require gradients are refused where gradients are recorded.
 """
 from __future__ import annotations
 
@@ -25,6 +26,12 @@ DTYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
 def _need(ok, what: str) -> None:
     if not ok:
         raise ValueError(what)
+
+
+def _no_grad(what: str) -> None:
+    """For tensors that require gradients: a result without its gradient is refused rather than returned."""
+    if torch.is_grad_enabled():
+        raise ValueError(f"{what} has no backward pass: call it under torch.no_grad(), or with detached tensors")
 
 
 def _ints(t, n: int, name: str, dev) -> int:
@@ -213,6 +220,8 @@ def shared_attention(q, k, v, table, lens, prefix_pages=None, prefix_len=None, s
     if q.dim() != 4 or k.dim() != 4 or k.shape != v.shape or k.stride() != v.stride():
         raise ValueError("q: [batch][tokens][heads][head_dim]; k and v: [pages][kv heads][page][head_dim] of one shape "
                          "and strides")
+    if q.requires_grad or k.requires_grad or v.requires_grad:
+        _no_grad("shared_attention")
     B, T, nq, d = q.shape
     n_pages, nkv, page, dk = k.shape
     dev, dtype = q.device, q.dtype
@@ -266,6 +275,8 @@ def token_probs(logits, temperature=None, out=None, stream=None):
     """softmax(logits / temperature) in 32 bits: logits [rows][vocab] (float, bf16 or fp16), temperature float [rows]
     or None (1).  Temperature 0 puts everything on the first of the largest logits."""
     _need(logits.dim() == 2 and logits.stride(1) == 1 and logits.dtype in DTYPES, "logits: [rows][vocab], rows contiguous")
+    if logits.requires_grad or (temperature is not None and temperature.requires_grad):
+        _no_grad("token_probs")
     n, V = logits.shape
     dev = logits.device
     t = None
@@ -294,6 +305,8 @@ def verify(target, draft, tokens, u, n_drafted=None, status=None, stream=None):
     or None (all).  Returns (tokens int32 [batch][drafted + 1], -1 after the sampled one; accepted int32 [batch])."""
     _need(target.dim() == 3 and target.dtype is torch.float32 and target.stride(2) == 1,
           "target: float [batch][drafted + 1][vocab], rows contiguous")
+    if target.requires_grad or (draft is not None and draft.requires_grad):
+        _no_grad("verify")
     B, T, V = target.shape
     T -= 1
     dev = target.device

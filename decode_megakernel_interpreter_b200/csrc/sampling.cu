@@ -356,6 +356,8 @@ constexpr int kVerThreads = 256;
 constexpr int kSeg = 512;  // values that a warp sums at a time: 16 per lane, in four runs of 128
 constexpr int kVerCluster = 8;
 constexpr int kMaxDrafted = 64;
+constexpr int kMaxVerVocab = 104857600;  // its running sums take 200 KB of a block
+static_assert((kMaxVerVocab / kSeg + kVerCluster - 1) / kVerCluster * sizeof(double) == 200 * 1024, "running sums");
 
 struct Weights {  // the values r that the new token is drawn by
   const float *p, *q;
@@ -623,7 +625,7 @@ extern "C" int mk_verify(const mk_verify_args *a, void *stream) {
     return MK_ERR_INVALID_ARG;
   const int C = kVerCluster;
   const size_t smem = ((size_t)(a->vocab + kSeg - 1) / kSeg + C - 1) / C * sizeof(double);
-  if (smem > 200 * 1024) return MK_ERR_UNSUPPORTED_SHAPE;
+  if (a->vocab > kMaxVerVocab) return MK_ERR_UNSUPPORTED_SHAPE;
   static std::atomic<uint64_t> allowed;
   int rc = smem > 40 * 1024 ? serve_allow_smem(allowed, (const void *)verify_kernel, 200 * 1024) : MK_OK;
   if (rc) return rc;

@@ -208,6 +208,7 @@ int mk_attn_shared(const mk_attn_shared_args *a, void *workspace, void *stream);
  *  - A logit of -infinity is a token that cannot come.  A row without a finite
  *    largest logit, with a NaN, or with a temperature that is negative or not
  *    finite has no distribution: its probabilities are all 0.
+ *  - n <= 2^24, vocab < 2^30.  Errors: MK_ERR_INVALID_ARG, MK_ERR_LAUNCH, MK_ERR_CUDA.
  */
 int mk_token_probs(const void *logits, int32_t dtype, int64_t logits_stride, const float *temperature,
                    float *probs, int64_t probs_stride, int32_t n, int32_t vocab, void *stream);
@@ -235,7 +236,10 @@ int mk_token_probs(const void *logits, int32_t dtype, int64_t logits_stride, con
  *  - out_tokens: device int32 [batch][max_drafted + 1]: the tokens that stand,
  *    the sampled one, then -1.  A row r that is 0 everywhere has no token: -1.
  *  - n_accepted: device int32 [batch]: a.
- *  - batch <= 65535, max_drafted 0 .. 64, vocab < 2^30.
+ *  - batch <= 65535, max_drafted 0 .. 64, vocab < 2^30.  A vocabulary above
+ *    104857600 is MK_ERR_UNSUPPORTED_SHAPE (a block keeps the running sums of its
+ *    part of a row on chip).
+ *  - Errors: MK_ERR_INVALID_ARG, MK_ERR_UNSUPPORTED_SHAPE, MK_ERR_LAUNCH, MK_ERR_CUDA.
  */
 typedef struct {
   int32_t batch;

@@ -95,3 +95,21 @@ def test_residuals_on_borders(V):
         v = [int(y * 2.0 ** 149) for y in w[row, at].astype(np.float64)]
         k, total = int(np.searchsorted(at, i)), sum(v)
         assert sum(v[:k + 1]) >= 0.5 * total - EPS * total and sum(v[:k]) <= 0.5 * total + EPS * total, i
+
+
+def test_the_largest_vocabulary():
+    """104857600 tokens: weights in a few places; the additions of a block's 25600 segments are 800 more."""
+    V = 104857600
+    at = [0, 511, 512, 13107199, 13107200, 60000001, 104857088, 104857599]
+    w = [3, 1, 4, 1, 5, 9, 2, 6]
+    p = torch.zeros(1, 1, V, device="cuda")
+    p[0, 0, at] = torch.tensor(w, dtype=torch.float32, device="cuda") / 32
+    for u in np.linspace(0, 0.999, 23).astype(np.float32):  # (exact sums)
+        tok, acc = sv.verify(p, None, torch.zeros(1, 0, dtype=torch.int32, device="cuda"), torch.tensor([[float(u)]], device="cuda"))
+        assert tok.item() == at[int(np.argmax(np.cumsum(w) > float(u) * sum(w)))] and acc.item() == 0
+    p.uniform_()
+    total = p.double().sum()
+    tok, acc = sv.verify(p, None, torch.zeros(1, 0, dtype=torch.int32, device="cuda"), torch.tensor([[0.7]], device="cuda"))
+    i, goal, slack = tok.item(), float(np.float32(0.7)) * float(total), (64 + 800) * 2.0 ** -53 * float(total)
+    c = p[0, 0, :i + 1].double().cumsum(0)  # (its own additions, as many as tokens, are off by V 2^-53 at most)
+    assert c[i] >= goal - slack - V * 2.0 ** -53 * float(total) and c[i - 1] <= goal + slack + V * 2.0 ** -53 * float(total)

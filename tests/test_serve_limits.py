@@ -1,0 +1,21 @@
+"""Limits that the header names, where no GPU is needed to be told of them."""
+import ctypes
+import os
+
+import pytest
+
+import decode_megakernel_interpreter_b200 as mk
+
+P = 256
+HEADER = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "include", "mk_serve.h")
+
+
+@pytest.mark.parametrize("vocab, code", [(104857601, mk.MK_ERR_UNSUPPORTED_SHAPE), ((1 << 30) - 1, mk.MK_ERR_UNSUPPORTED_SHAPE),
+                                         (1 << 30, mk.MK_ERR_INVALID_ARG)])
+def test_verification_of_too_large_a_vocabulary(vocab, code):
+    a = mk.mk_verify_args(batch=1, vocab=vocab, target=P, u=P, out_tokens=P, n_accepted=P, target_batch_stride=vocab,
+                          target_row_stride=vocab)
+    assert mk.load().mk_verify(ctypes.byref(a), None) == code
+    text = open(HEADER).read()
+    part = text[text.index(" * mk_verify:"):text.index("} mk_verify_args;")]
+    assert "104857600" in part and "MK_ERR_UNSUPPORTED_SHAPE" in part

@@ -77,11 +77,19 @@ def peaks():
         return FALLBACK_HBM_GBS, "fallback"
 
 
+# the serving operators' own sources, which no step of the bench launches
+SERVING = ("kv_pages.cu", "sampling.cu", "serve_common.h", "shared_attn.cu")
+
+
+def step_sources() -> list:
+    """The sources that the decode step's kernels, plans and launches are made from."""
+    return [f for f in sorted(os.listdir(os.path.join(ROOT, "decode_megakernel_interpreter_b200", "csrc"))) if f not in SERVING]
+
+
 def src_hash() -> str:
-    """Of the sources that the decode step's kernels and plans are made from."""
     h = hashlib.sha256()
     csrc = os.path.join(ROOT, "decode_megakernel_interpreter_b200", "csrc")
-    for f in sorted(f for f in os.listdir(csrc) if f.startswith(("interp", "mk_internal", "planner"))):
+    for f in step_sources():
         with open(os.path.join(csrc, f), "rb") as fh:
             h.update(f.encode() + fh.read())
     return h.hexdigest()[:16]

@@ -3,8 +3,8 @@
 // Each call is one block that does the bookkeeping -- it holds a list entry
 // per thread and the page bitmap in shared memory, and orders everything by
 // prefix sums, so the result does not depend on the order of atomics -- and a
-// grid-wide kernel that moves the rows the bookkeeping listed, which is
-// scheduled while the bookkeeping still runs.  The bookkeeping is bound by the
+// grid-wide kernel that moves the rows the bookkeeping listed, whose blocks
+// start as soon as the bookkeeping's one is done.  The bookkeeping is bound by the
 // latency of its few dependent steps: 16 sequences resized in 11.6 us and 15
 // forked in 10.4 us, both kernels included (captured, B200).
 #include "serve_common.h"
@@ -361,7 +361,9 @@ struct PoolDev {
 };
 
 // Entry i of a caller's list may be copied: in range, and its rows written by
-// no earlier entry and read by none.  One block per entry.
+// no earlier entry and read by none.  One block per entry, which looks at all the
+// others (a call with entries of one row, 2 layers of 2 heads: 8.1 us for 125
+// entries, 12.2 for 1024, 447 for 16384).
 __global__ void __launch_bounds__(256) check_copy_kernel(const Job *items, int n, PoolDev a, PoolDev b, int *good,
                                                          int32_t *status) {
   pdl_wait();

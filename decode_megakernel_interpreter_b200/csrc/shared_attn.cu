@@ -562,7 +562,7 @@ __device__ __forceinline__ int small_items(const AttnDev &p, char *sm, int *red)
         }
       }
       // ---- p as two numbers of the operands' type, so that its rounding
-      // (2^-9 or 2^-12 relative) does not show beside the output's own
+      // (2^-8 or 2^-11 relative as one) does not show beside the output's own
       uint32_t ph[4], pl[4];
 #pragma unroll
       for (int n = 0; n < 2; ++n)

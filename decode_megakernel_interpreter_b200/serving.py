@@ -5,11 +5,13 @@ probabilities and the verification of drafted tokens.
 Argument checks and marshalling only; the work runs in libmk.so.  Every call
 is asynchronous on the current stream of its tensors' device (or on `stream`),
 takes its scratch from torch's allocator on that stream, and can be captured
-into a CUDA graph.  Tensors of one call are on one device, which need not be
-the current one.  Arguments that do not fit raise ValueError, codes of the
-library MkError.  An empty list or batch is a call without work: it returns its
-(empty) outputs and launches nothing.  There are no backward passes: tensors
-that require gradients are refused where gradients are recorded.
+into a CUDA graph.  With `stream`, the caller orders it with the streams that
+make the inputs and use the outputs, and keeps the inputs until the call has
+run.  Tensors of one call are on one device, which need not be the current one.
+Arguments that do not fit raise ValueError, codes of the library MkError.  An
+empty list or batch is a call without work: it returns its (empty) outputs and
+launches nothing.  There are no backward passes: tensors that require gradients
+are refused where gradients are recorded.
 """
 from __future__ import annotations
 
@@ -216,7 +218,8 @@ def shared_attention(q, k, v, table, lens, prefix_pages=None, prefix_len=None, s
     q: [batch][tokens][q heads][head_dim] bf16 / fp16 (tokens: the last positions of each sequence); k, v: one layer of
     a pool, [pages][kv heads][page][head_dim]; table: int32 [batch][pages of a sequence]; lens: int32 [batch], prefix
     included (negative: the sequence is unused and its output rows stay as they are); prefix_pages: int32 pages of the
-    prefix; prefix_len: int32, one word.  Returns out like q, or (out, lse) with lse float [batch][tokens][q heads]."""
+    prefix; prefix_len: int32, one word.  Returns out like q, or (out, lse) with lse float [batch][tokens][q heads].
+    Sums are 32-bit; a softmax weight is rounded to q's type where prefix_pages has room for 1024 positions or more."""
     if q.dim() != 4 or k.dim() != 4 or k.shape != v.shape or k.stride() != v.stride():
         raise ValueError("q: [batch][tokens][heads][head_dim]; k and v: [pages][kv heads][page][head_dim] of one shape "
                          "and strides")

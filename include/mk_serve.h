@@ -153,6 +153,15 @@ enum { MK_DTYPE_BF16 = 0, MK_DTYPE_F16 = 1, MK_DTYPE_F32 = 2 };
  *  - MK_ERR_TIMEOUT in *status: a wait inside the kernel gave up after a second
  *    (every one is bounded); the results are then undefined.
  *  - Results do not depend on timing: the same call gives the same bits.
+ *  - Scores, maxima and sums are 32-bit.  The weights p go to the matrix
+ *    instructions in the type of q: as one number each (off by 2^-8 of it for
+ *    bf16, 2^-11 for fp16, like out's own rounding) for a prefix whose pages have
+ *    room for 1024 positions or more, as two (2^-16, 2^-22) for other prefixes and
+ *    for a sequence's own positions.  fp16 weights less than 2^-21 of the row's
+ *    largest are off by up to 2^-32 of that.
+ *  - Each page list has room for fewer than 2^31 - 64 positions, and n_kv_heads *
+ *    (batch * n_tokens * group / 16 + batch) * (the room of both lists / 16 + 6)
+ *    stays below 2^31: MK_ERR_INVALID_ARG.
  */
 typedef struct {
   int32_t batch;              /* 1 .. 1024; batch * n_tokens <= 1024 */

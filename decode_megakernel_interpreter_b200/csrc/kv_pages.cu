@@ -472,13 +472,24 @@ bool state_ok(const mk_kv_state *s) {
   return s && s->words && aligned_to(s->words, 16) && s->n_seqs > 0 && s->n_seqs <= (1 << 20) && s->max_pages > 0 &&
          s->n_pages > 0 && s->n_pages <= kMaxPages;
 }
-bool both_ok(const mk_kv_pool *p, const mk_kv_state *s) {
-  return pool_ok(p) && state_ok(s) && p->n_pages == s->n_pages && (long long)s->max_pages * p->page < (1ll << 31);
-}
 size_t pool_bytes(const mk_kv_pool &p) {
   return (size_t)p.n_layers * p.n_pages * p.n_kv_heads * p.page * p.head_dim * p.elem_bytes;
 }
 PoolDev dev(const mk_kv_pool &p) { return PoolDev{(char *)p.k, (char *)p.v, p.n_pages, p.page}; }
+
+// Pieces that a job's rows of one head are moved in, and warps' units of a job.
+int piece_rows_of(const mk_kv_pool &p) { return std::max(1, kPieceBytes / (p.head_dim * p.elem_bytes)); }
+int pieces_of(const mk_kv_pool &a, const mk_kv_pool &b) {
+  return (std::min(a.page, b.page) + piece_rows_of(a) - 1) / piece_rows_of(a);
+}
+// They are counted in 32 bits.
+bool units_ok(const mk_kv_pool &a, const mk_kv_pool &b) {
+  return (long long)a.n_layers * 2 * a.n_kv_heads * pieces_of(a, b) < 1ll << 31;
+}
+bool both_ok(const mk_kv_pool *p, const mk_kv_state *s) {
+  return pool_ok(p) && state_ok(s) && p->n_pages == s->n_pages && (long long)s->max_pages * p->page < (1ll << 31) &&
+         units_ok(*p, *p);
+}
 
 // The grid that moves the listed rows (max_jobs: as many as there can be).
 int launch_move(const mk_kv_pool &a, const mk_kv_pool &b, const Job *jobs, const int *count, int n, const int *good,
@@ -486,10 +497,8 @@ int launch_move(const mk_kv_pool &a, const mk_kv_pool &b, const Job *jobs, const
   int sms = 0, rc = serve_sms(&sms);
   if (rc) return rc;
   const int row_bytes = a.head_dim * a.elem_bytes;
-  const int piece_rows = std::max(1, kPieceBytes / row_bytes);
-  const int pieces = (std::min(a.page, b.page) + piece_rows - 1) / piece_rows;
-  const long long per_job = (long long)a.n_layers * 2 * a.n_kv_heads * pieces, units = per_job * n;
-  if (per_job >= 1ll << 31) return MK_ERR_INVALID_ARG;
+  const int piece_rows = piece_rows_of(a), pieces = pieces_of(a, b);
+  const long long units = (long long)a.n_layers * 2 * a.n_kv_heads * pieces * n;
   const long long blocks = (units + kCopyThreads / 32 - 1) / (kCopyThreads / 32);
   const int grid = (int)std::max<long long>(1, std::min<long long>(blocks, (long long)sms * 8));
   return serve_launch(move_kernel, dim3(grid), kCopyThreads, 0, st, true, 1, jobs, count, n, good, dev(a), dev(b),
@@ -566,7 +575,7 @@ extern "C" int mk_kv_copy(const mk_kv_pool *src, const mk_kv_pool *dst, const in
   if (!pool_ok(src) || !pool_ok(dst) || !items || n < 1 || n > kMaxCopy || !workspace || !aligned_to(workspace, 256))
     return MK_ERR_INVALID_ARG;
   if (src->n_layers != dst->n_layers || src->n_kv_heads != dst->n_kv_heads || src->head_dim != dst->head_dim ||
-      src->elem_bytes != dst->elem_bytes)
+      src->elem_bytes != dst->elem_bytes || !units_ok(*src, *dst))
     return MK_ERR_INVALID_ARG;
   const bool same = src->k == dst->k && src->v == dst->v && src->n_pages == dst->n_pages && src->page == dst->page;
   if (!same) {  // else every pair of buffers is apart

@@ -43,6 +43,7 @@ typedef struct {
   int32_t page;       /* positions per page, 1 .. 2^24 */
   int32_t head_dim;
   int32_t elem_bytes; /* 1, 2 or 4; head_dim * elem_bytes must be a multiple of 16 */
+  /* n_layers * n_kv_heads * ceil(page / rows of 8 KB) is below 2^30 */
 } mk_kv_pool;
 
 /*

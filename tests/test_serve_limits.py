@@ -19,3 +19,15 @@ def test_verification_of_too_large_a_vocabulary(vocab, code):
     text = open(HEADER).read()
     part = text[text.index(" * mk_verify:"):text.index("} mk_verify_args;")]
     assert "104857600" in part and "MK_ERR_UNSUPPORTED_SHAPE" in part
+
+
+@pytest.mark.parametrize("layers, heads, page", [(65536, 16384, 1), (65536, 65536, 1), (4096, 1024, 1 << 18)])
+def test_pools_whose_rows_cannot_be_counted(layers, heads, page):
+    """Refused before anything is launched: a call must not change the bookkeeping and then fail to move the rows."""
+    pool = mk.mk_kv_pool(P, P, layers, 1, heads, page, 16, 1)
+    st = mk.mk_kv_state(P, 2, 1, 1)
+    p, s, L = ctypes.byref(pool), ctypes.byref(st), mk.load()
+    assert L.mk_kv_resize(p, s, P, P, 1, P, None) == mk.MK_ERR_INVALID_ARG
+    assert L.mk_kv_fork(p, s, P, P, 1, P, None) == mk.MK_ERR_INVALID_ARG
+    assert L.mk_kv_compact(p, s, P, None) == mk.MK_ERR_INVALID_ARG
+    assert L.mk_kv_copy(p, p, P, 1, None, P, None) == mk.MK_ERR_INVALID_ARG

@@ -315,6 +315,7 @@ def verify(target, draft, tokens, u, n_drafted=None, status=None, stream=None):
     dev = target.device
     _need(T >= 0 and u.shape == (B, T + 1) and u.dtype is torch.float32 and u.is_contiguous() and u.device == dev,
           "u: a contiguous float tensor [batch][drafted + 1]")
+    _need(tokens.dim() != 2 or T == 0 or tokens.shape[1] == T, "tokens: [batch][drafted]")  # (or the words in a row)
     d, ds = None, (0, 0)
     if draft is not None and T > 0:
         _need(draft.shape == (B, T, V) and draft.dtype is torch.float32 and draft.stride(2) == 1 and draft.device == dev,

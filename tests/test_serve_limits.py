@@ -3,8 +3,10 @@ import ctypes
 import os
 
 import pytest
+import torch
 
 import decode_megakernel_interpreter_b200 as mk
+from decode_megakernel_interpreter_b200 import serving as sv
 
 P = 256
 HEADER = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "include", "mk_serve.h")
@@ -31,3 +33,14 @@ def test_pools_whose_rows_cannot_be_counted(layers, heads, page):
     assert L.mk_kv_fork(p, s, P, P, 1, P, None) == mk.MK_ERR_INVALID_ARG
     assert L.mk_kv_compact(p, s, P, None) == mk.MK_ERR_INVALID_ARG
     assert L.mk_kv_copy(p, p, P, 1, None, P, None) == mk.MK_ERR_INVALID_ARG
+
+
+def test_rows_of_tokens_that_are_not_the_drafts():
+    """A longer buffer's rows would be read as if they followed one another."""
+    p, u = torch.zeros(2, 3, 10), torch.zeros(2, 3)
+    for shape in ((2, 3), (2, 4), (4, 1), (1, 4)):
+        with pytest.raises(ValueError, match="tokens"):
+            sv.verify(p, None, torch.zeros(shape, dtype=torch.int32), u)
+    for shape in ((2, 2), (4,), (3, 2)):
+        with pytest.raises(ValueError, match="CUDA"):  # taken, but for the device
+            sv.verify(p, None, torch.zeros(shape, dtype=torch.int32), u)
